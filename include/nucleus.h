@@ -90,6 +90,8 @@ extern "C" {
 /* Logit element types. */
 #define NUCLEUS_F32 0
 #define NUCLEUS_BF16 1
+#define NUCLEUS_F16 2 /* nucleus_project and nucleus_sample_given only (since version 270) */
+#define NUCLEUS_F64 3 /* uniforms of the *_given entry points only (since version 270) */
 
 typedef struct nucleus_options {
     int32_t dtype;               /* NUCLEUS_F32 (default) or NUCLEUS_BF16 */
@@ -283,6 +285,61 @@ int nucleus_sample_rejection(const void* logits, int64_t B, int64_t V, const flo
 int nucleus_spec_verify(const float* target_probs, const float* draft_probs, const int32_t* draft_token,
                         int64_t B, int64_t V, uint64_t seed, uint64_t step, int32_t* out_token,
                         int32_t* out_accepted, const nucleus_options* opt);
+
+/* Activations of nucleus_project (z is the product plus the bias). */
+#define NUCLEUS_ACT_NONE 0
+#define NUCLEUS_ACT_RELU 1    /* max(z, 0); NaN stays NaN */
+#define NUCLEUS_ACT_GELU 2    /* z Phi(z), Phi the normal distribution function */
+#define NUCLEUS_ACT_SILU 3    /* z / (1 + exp(-z)) */
+#define NUCLEUS_ACT_SOFTCAP 4 /* c tanh(z / c), c = softcap > 0 and finite */
+
+typedef struct nucleus_project_options {
+    int32_t dtype;           /* of hidden and weight: NUCLEUS_F32 (default), NUCLEUS_BF16 or NUCLEUS_F16 */
+    int32_t out_dtype;       /* NUCLEUS_F32 (default) or dtype */
+    int32_t activation;      /* NUCLEUS_ACT_* */
+    float softcap;           /* c of NUCLEUS_ACT_SOFTCAP; ignored otherwise */
+    void* stream;            /* hipStream_t to launch on; NULL = the null stream */
+    const void* bias;        /* optional device [N] */
+    const void* residual;    /* optional device [M, N]; may be `out` itself, of the same type and stride */
+    int32_t bias_dtype;      /* NUCLEUS_F32 or dtype */
+    int32_t residual_dtype;  /* NUCLEUS_F32 or dtype */
+    int64_t hidden_stride;   /* elements between row starts; 0 means K */
+    int64_t weight_stride;   /* 0 means K */
+    int64_t out_stride;      /* 0 means N */
+    int64_t residual_stride; /* 0 means N */
+} nucleus_project_options;
+
+/*
+ * The product that makes logits, with its epilogue in the same kernel (since
+ * version 270):
+ *
+ *   out[m, n] = act( sum_k hidden[m, k] weight[n, k] + bias[n] ) + residual[m, n]
+ *
+ * A vocabulary projection (weight [V, K], with a soft cap, and a residual
+ * that carries per-request logit biases or an additive mask, -inf forbidding
+ * a token: the logits the sampling calls take, "Top-p (Nucleus) Sampling, in
+ * depth", "Where top-p sits in the sampler chain"), or the block of a draft
+ * head (x + silu(W x + b)) whose proposals nucleus_spec_verify judges.
+ *
+ * hidden    device, [M, hidden_stride] elements of dtype; read only.
+ * weight    device, [N, weight_stride] elements of dtype, rows along k; read only.
+ * M, N, K   0 <= M, N < 2^31, 1 <= K < 2^31; M == 0 or N == 0 returns
+ *           NUCLEUS_OK and launches nothing.
+ * out       device, [M, out_stride] elements of out_dtype; the elements
+ *           between rows are left as they were.  It may not overlap hidden,
+ *           weight or bias, nor residual except as that field says.
+ * opt       NULL for all defaults (fp32, no epilogue, dense, null stream).
+ *
+ * Sums and the epilogue are held in fp32 and rounded once, to nearest even.
+ * The order in which k is summed is fixed for given sizes, types and
+ * alignment, so equal calls give equal bits.  Rows that start on 16-byte
+ * boundaries and are whole multiples of 16 bytes long take the fast kernels;
+ * any other layout gives the same result more slowly.  Elements of hidden
+ * and weight past a row's K are never used.  No workspace.  Returns
+ * NUCLEUS_OK or a negative code; asynchronous on opt->stream.
+ */
+int nucleus_project(const void* hidden, const void* weight, int64_t M, int64_t N, int64_t K, void* out,
+                    const nucleus_project_options* opt);
 
 /* Device workspace, in bytes, that nucleus_spec_verify needs: 8 bytes per
  * 8192-token chunk of every row.  0 for invalid shapes. */

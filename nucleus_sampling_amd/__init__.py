@@ -13,18 +13,20 @@ The C ABI, with the semantics of every argument, is ``include/nucleus.h``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
 
 import torch
 
-__all__ = ["sample", "sample_rejection", "RejectionResult", "spec_verify", "SpecResult", "workspace_bytes", "strerror", "version", "stream_read", "NucleusError", "lib", "LIB_PATH"]
+__all__ = ["sample", "sample_rejection", "RejectionResult", "spec_verify", "SpecResult", "project", "workspace_bytes", "strerror", "version", "stream_read", "NucleusError", "lib", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnucleus.so")
 
 NUCLEUS_F32 = 0
 NUCLEUS_BF16 = 1
+NUCLEUS_F16 = 2  # project and sample_given only
 NUCLEUS_FLAG_SINGLE_WORKGROUP = 1
 NUCLEUS_FLAG_SPLIT_ROWS = 2
 NUCLEUS_FLAG_ROW_RACE = 4
@@ -55,6 +57,24 @@ class _Options(ctypes.Structure):
     ]
 
 
+class _ProjectOptions(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("softcap", ctypes.c_float),
+        ("stream", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("bias_dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+        ("hidden_stride", ctypes.c_int64),
+        ("weight_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -78,6 +98,8 @@ def lib():
         L.nucleus_spec_verify.restype = ctypes.c_int
         L.nucleus_spec_workspace_bytes.argtypes = [i64, i64]
         L.nucleus_spec_workspace_bytes.restype = ctypes.c_size_t
+        L.nucleus_project.argtypes = [vp, vp, i64, i64, i64, vp, ctypes.POINTER(_ProjectOptions)]
+        L.nucleus_project.restype = ctypes.c_int
         L.nucleus_workspace_bytes.argtypes = [i64, i64, ctypes.c_int32]
         L.nucleus_workspace_bytes.restype = ctypes.c_size_t
         L.nucleus_workspace_bytes_for.argtypes = [i64, i64, ctypes.c_int32, ctypes.c_int32]
@@ -357,6 +379,110 @@ def spec_verify(target_probs: torch.Tensor, draft_probs: torch.Tensor, draft_tok
                                    out.token.data_ptr() if B else None, out.accepted.data_ptr() if B else None,
                                    ctypes.byref(opt))
     _check(rc, "nucleus_spec_verify")
+    return out
+
+
+_CODES = {torch.float32: NUCLEUS_F32, torch.bfloat16: NUCLEUS_BF16, torch.float16: NUCLEUS_F16}
+_ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "softcap": 4}
+_NO_SCOPE = contextlib.nullcontext()
+
+
+def _scope(dev, stream):
+    """(stream, context): the stream a call launches on, and a context under
+    which the call's own allocations and conversions are made on that stream
+    and device (a no-op when they are the current ones)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+        if dev.index == torch.cuda.current_device():
+            return stream, _NO_SCOPE
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return stream, torch.cuda.stream(stream)
+
+
+def _no_grad(name, *tensors):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise NucleusError(f"{name} is for inference: it has no backward pass; call it under torch.no_grad() or detach its inputs")
+
+
+def _matrix(t, name, dev=None):
+    """Check that ``t`` is a 2-D GPU tensor (on ``dev``) with a dense last
+    dimension; rows that overlap or repeat are copied apart."""
+    if not torch.is_tensor(t) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if not t.is_cuda:
+        raise NucleusError(f"{name} must be on the GPU: this library has no CPU path")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.contiguous() if rows > 1 and t.stride(0) < cols else t
+
+
+def project(hidden: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+            residual: Optional[torch.Tensor] = None, *, activation: str = "none", softcap: float = 0.0,
+            out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``act(hidden @ weight.T + bias) + residual`` in one kernel
+    (``nucleus_project``): a vocabulary projection that makes logits, or the
+    block of a draft head.
+
+    ``hidden`` [M, K] and ``weight`` [N, K] share one type (float32, bfloat16
+    or float16); ``bias`` [N] and ``residual`` [M, N] have that type or
+    float32; the output is ``out_dtype`` (default: that type; float32 is the
+    other choice).  ``activation`` is "none", "relu", "gelu", "silu" or
+    "softcap" (``softcap * tanh(z / softcap)``).  Rows may be strided, the
+    last dimensions must be dense.  ``out`` may supply the output, and may be
+    ``residual`` itself.  Launches on ``stream`` (default: the current
+    stream) and returns without synchronising.  Inference only: inputs that
+    autograd would have to follow are refused."""
+    dev = hidden.device
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}, got {activation!r}")
+    if hidden.dtype not in _CODES:
+        raise TypeError(f"hidden must be float32, bfloat16 or float16, got {hidden.dtype}")
+    if weight.dtype != hidden.dtype:
+        raise TypeError(f"weight must have hidden's type {hidden.dtype}, got {weight.dtype}")
+    _no_grad("project", hidden, weight, bias, residual)
+    if not hidden.is_cuda:
+        raise NucleusError("hidden must be on the GPU: this library has no CPU path")
+    with _scope(dev, stream)[1]:
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        hidden, weight = _matrix(hidden, "hidden"), _matrix(weight, "weight", dev)
+        M, K = hidden.shape
+        N = weight.shape[0]
+        if weight.shape[1] != K or K < 1:
+            raise ValueError(f"hidden {tuple(hidden.shape)} and weight {tuple(weight.shape)} must share K >= 1")
+        opt = _ProjectOptions()
+        opt.dtype = _CODES[hidden.dtype]
+        opt.activation = _ACTIVATIONS[activation]
+        opt.softcap = softcap
+        opt.stream = s.cuda_stream
+        if bias is not None:
+            if bias.shape != (N,) or bias.device != dev or bias.dtype not in (hidden.dtype, torch.float32):
+                raise ValueError(f"bias must be a [{N}] tensor of {hidden.dtype} or float32 on {dev}")
+            bias = bias.contiguous()
+            opt.bias, opt.bias_dtype = bias.data_ptr(), _CODES[bias.dtype]
+        if out is None:
+            out = torch.empty((M, N), dtype=hidden.dtype if out_dtype is None else out_dtype, device=dev)
+        elif out.shape != (M, N) or out.device != dev or (out_dtype is not None and out.dtype != out_dtype) or (
+                N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
+            raise ValueError(f"out must be a [{M}, {N}] tensor on {dev}, of out_dtype and with rows apart and dense")
+        if out.dtype not in (hidden.dtype, torch.float32):
+            raise TypeError(f"the output must be {hidden.dtype} or float32, got {out.dtype}")
+        opt.out_dtype = _CODES[out.dtype]
+        if residual is not None:
+            if residual.dtype not in (hidden.dtype, torch.float32) or residual.shape != (M, N):
+                raise ValueError(f"residual must be a [{M}, {N}] tensor of {hidden.dtype} or float32")
+            residual = _matrix(residual, "residual", dev)
+            opt.residual, opt.residual_dtype = residual.data_ptr(), _CODES[residual.dtype]
+            opt.residual_stride = residual.stride(0) if M > 1 else N
+        opt.hidden_stride = hidden.stride(0) if M > 1 else K
+        opt.weight_stride = weight.stride(0) if N > 1 else K
+        opt.out_stride = out.stride(0) if M > 1 else N
+        rc = lib().nucleus_project(hidden.data_ptr(), weight.data_ptr(), M, N, K, out.data_ptr(), ctypes.byref(opt))
+    _check(rc, "nucleus_project")
     return out
 
 

@@ -2,14 +2,13 @@
 // argument validation, launch-shape choice and launches on the caller's
 // stream.  No call synchronises the device or allocates memory.
 #include <hip/hip_runtime.h>
-#include <string.h>
-
 #include <atomic>
 #include <chrono>
 #include <mutex>
 
 #include "nucleus.h"
 #include "common.h"
+#include "host.h"
 #include "params.h"
 #include "rejection.h"
 #include "rowpath.h"
@@ -21,24 +20,6 @@
 using namespace nucleus;
 
 namespace {
-
-// The library is built for gfx950 only; refuse other devices up front rather
-// than fail inside a launch.
-int check_device()
-{
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return NUCLEUS_EDEVICE;
-    static std::mutex mu;
-    static int known[64] = {0};  // 0 unknown, 1 ok, -1 unsupported
-    if (dev < 0 || dev >= 64) return NUCLEUS_EDEVICE;
-    std::lock_guard<std::mutex> lock(mu);
-    if (known[dev] == 0) {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return NUCLEUS_EDEVICE;
-        known[dev] = (strncmp(prop.gcnArchName, "gfx950", 6) == 0) ? 1 : -1;
-    }
-    return known[dev] == 1 ? NUCLEUS_OK : NUCLEUS_EDEVICE;
-}
 
 // By default a row runs on one workgroup of its own (row_kernel, every
 // phase).  Small batches of long rows split each row over ceil(V / kChunk)
@@ -119,12 +100,6 @@ int64_t race_workgroups(int32_t dtype)
     return k;
 }
 
-template <class T>
-bool aligned(const T* p)
-{
-    return ((uintptr_t)p % alignof(T)) == 0;
-}
-
 // Whether a call asks for the pre-chain (penalties or a grammar mask).
 bool has_prechain(const nucleus_options* opt)
 {
@@ -176,7 +151,7 @@ uint64_t* stamps_for(int64_t B)
 
 extern "C" {
 
-int nucleus_version(void) { return 260; }
+int nucleus_version(void) { return 270; }
 
 int nucleus_phase_stamps(uint64_t* buf, int64_t rows)
 {

@@ -7,6 +7,7 @@ namespace nucleus {
 
 constexpr int kF32 = 0;
 constexpr int kBF16 = 1;
+constexpr int kF16 = 2;  // project.h and given.h only
 
 struct Params {
     const void* logits;       // [B, stride] elements of the launch dtype
