@@ -341,6 +341,81 @@ typedef struct nucleus_project_options {
 int nucleus_project(const void* hidden, const void* weight, int64_t M, int64_t N, int64_t K, void* out,
                     const nucleus_project_options* opt);
 
+/*
+ * nucleus_sample's chain drawn from random numbers the caller brings (since
+ * version 270): the same kept set, then the inverse CDF in index order
+ * ("Top-p (Nucleus) Sampling, in depth", "Batched top-p with a different p
+ * per request", sample_top_p; "Implement batched top-p sampling with
+ * temperature", "A strong answer", sample), N independent draws per row from
+ * one distribution:
+ *
+ *   out_token[b, n] = the lowest kept i whose running sum of kept weights
+ *                     w_j, j <= i, exceeds uniforms[b, n] times their whole sum
+ *
+ * A uniform <= 0 draws the first and one >= 1 the last kept token of positive
+ * weight (the clamp of that page's sampler); NaN gives token -1 for that draw
+ * alone.  Greedy rows ignore the uniforms.  Masses are carried to about 1e-13
+ * relative, so keep counts and tokens are those of the float64 definition
+ * unless a sum falls that close to its border.
+ *
+ * logits .. min_p   as for nucleus_sample; opt->dtype may also be NUCLEUS_F16
+ *                   (widened exactly, as bf16).
+ * uniforms          device [B, N], contiguous, of uniform_dtype (NUCLEUS_F32 or NUCLEUS_F64).
+ * N                 draws per row, 1 <= N < 2^31.
+ * out_token         device [B, N] int32; -1 on a row error.
+ * out_keep_count    device [B] int32, as for nucleus_sample.
+ * out_token_logprob device [B, N] float, or NULL: ln of the drawn token's
+ *                   probability in the kept, renormalised distribution,
+ *                   (x - m)/T - ln S_keep; 0 for greedy rows, NaN where the token is -1.
+ * out_probs         device [B, V] float, or NULL, as for nucleus_sample.
+ * opt               NULL, or options with dtype, stream and row_stride used;
+ *                   flags, seeds, out_min_kept_logit, out_logprobs, the
+ *                   pre-chain and split_give_up_row must be unset
+ *                   (NUCLEUS_EINVAL otherwise).
+ *
+ * Returns NUCLEUS_OK or a negative code; asynchronous on opt->stream, and
+ * may be captured into a graph.  Results do not depend on the rest of the
+ * batch and equal calls give equal bits.  No workspace.
+ */
+int nucleus_sample_given(const void* logits, int64_t B, int64_t V, const float* temperature, const float* top_p,
+                         const int32_t* top_k, const float* min_p, const void* uniforms, int32_t uniform_dtype,
+                         int64_t N, int32_t* out_token, int32_t* out_keep_count, float* out_token_logprob,
+                         float* out_probs, const nucleus_options* opt);
+
+/*
+ * nucleus_spec_verify from random numbers the caller brings (since version
+ * 270): row b accepts its draft token d iff u0 q(d) < p(d), u0 =
+ * uniforms[b, 0], and else draws by the inverse CDF in index order from
+ * r_i = max(p_i - q_i, 0): the lowest i whose running sum of r exceeds
+ * u1 = uniforms[b, 1] times their whole sum (u1 <= 0 the first, u1 >= 1 the
+ * last i with r_i > 0).  Products and sums are taken in double.
+ *
+ * target_probs, draft_probs, draft_token   as for nucleus_spec_verify; the
+ *               probabilities are finite and not negative (a NaN accepts
+ *               nothing and adds nothing).
+ * uniforms      device [B, 2], contiguous, of uniform_dtype (NUCLEUS_F32 or NUCLEUS_F64).
+ * out_token     device [B] int32: d if accepted, else the residual draw; -1 if
+ *               d is outside [0, V), if u0, or for a rejected row u1, is NaN,
+ *               or if the sum of r is 0 or not finite.
+ * out_accepted  device [B] int32, or NULL.
+ * opt           required for B > 0: stream and the workspace (at least
+ *               nucleus_spec_given_workspace_bytes(B, V) bytes, 256-byte
+ *               aligned, no initial value needed; NUCLEUS_EWORKSPACE
+ *               otherwise) are used; dtype must be NUCLEUS_F32, row_stride 0
+ *               or V, everything else unset (NUCLEUS_EINVAL otherwise).
+ *
+ * Returns NUCLEUS_OK or a negative code.  Asynchronous on opt->stream, and
+ * may be captured into a graph; calls that may overlap need different
+ * workspaces.  An accepted row reads two floats.
+ */
+int nucleus_spec_verify_given(const float* target_probs, const float* draft_probs, const int32_t* draft_token,
+                              int64_t B, int64_t V, const void* uniforms, int32_t uniform_dtype, int32_t* out_token,
+                              int32_t* out_accepted, const nucleus_options* opt);
+
+/* Device workspace, in bytes, that nucleus_spec_verify_given needs: 8 bytes
+ * per 8192-token chunk of every row.  0 for invalid shapes. */
+size_t nucleus_spec_given_workspace_bytes(int64_t B, int64_t V);
+
 /* Device workspace, in bytes, that nucleus_spec_verify needs: 8 bytes per
  * 8192-token chunk of every row.  0 for invalid shapes. */
 size_t nucleus_spec_workspace_bytes(int64_t B, int64_t V);

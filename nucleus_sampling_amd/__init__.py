@@ -20,13 +20,14 @@ from typing import NamedTuple, Optional
 
 import torch
 
-__all__ = ["sample", "sample_rejection", "RejectionResult", "spec_verify", "SpecResult", "project", "workspace_bytes", "strerror", "version", "stream_read", "NucleusError", "lib", "LIB_PATH"]
+__all__ = ["sample", "sample_rejection", "RejectionResult", "spec_verify", "SpecResult", "project", "sample_given", "GivenResult", "spec_verify_given", "workspace_bytes", "strerror", "version", "stream_read", "NucleusError", "lib", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnucleus.so")
 
 NUCLEUS_F32 = 0
 NUCLEUS_BF16 = 1
 NUCLEUS_F16 = 2  # project and sample_given only
+NUCLEUS_F64 = 3  # uniforms of the *_given calls only
 NUCLEUS_FLAG_SINGLE_WORKGROUP = 1
 NUCLEUS_FLAG_SPLIT_ROWS = 2
 NUCLEUS_FLAG_ROW_RACE = 4
@@ -98,6 +99,13 @@ def lib():
         L.nucleus_spec_verify.restype = ctypes.c_int
         L.nucleus_spec_workspace_bytes.argtypes = [i64, i64]
         L.nucleus_spec_workspace_bytes.restype = ctypes.c_size_t
+        L.nucleus_sample_given.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, ctypes.c_int32, i64, vp, vp, vp, vp,
+                                           ctypes.POINTER(_Options)]
+        L.nucleus_sample_given.restype = ctypes.c_int
+        L.nucleus_spec_verify_given.argtypes = [vp, vp, vp, i64, i64, vp, ctypes.c_int32, vp, vp, ctypes.POINTER(_Options)]
+        L.nucleus_spec_verify_given.restype = ctypes.c_int
+        L.nucleus_spec_given_workspace_bytes.argtypes = [i64, i64]
+        L.nucleus_spec_given_workspace_bytes.restype = ctypes.c_size_t
         L.nucleus_project.argtypes = [vp, vp, i64, i64, i64, vp, ctypes.POINTER(_ProjectOptions)]
         L.nucleus_project.restype = ctypes.c_int
         L.nucleus_workspace_bytes.argtypes = [i64, i64, ctypes.c_int32]
@@ -484,6 +492,113 @@ def project(hidden: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
         rc = lib().nucleus_project(hidden.data_ptr(), weight.data_ptr(), M, N, K, out.data_ptr(), ctypes.byref(opt))
     _check(rc, "nucleus_project")
     return out
+
+
+class GivenResult(NamedTuple):
+    token: torch.Tensor              # int32, shaped as the uniforms; -1 on a row error or a NaN uniform
+    keep_count: torch.Tensor         # int32 [B]
+    logprob: torch.Tensor            # float32, shaped as the uniforms: of each drawn token
+    probs: Optional[torch.Tensor]    # float32 [B, V] or None
+
+
+def _uniforms(u, shapes, dev):
+    if not torch.is_tensor(u):
+        u = torch.as_tensor(u, dtype=torch.float64)
+    if u.dtype not in (torch.float32, torch.float64):
+        raise TypeError(f"uniforms must be float32 or float64, got {u.dtype}")
+    if tuple(u.shape) not in shapes and (u.dim() != 2 or (u.shape[0], None) not in shapes or u.shape[1] < 1):
+        raise ValueError(f"uniforms of shape {tuple(u.shape)} do not fit the batch")
+    return u.to(dev).contiguous(), NUCLEUS_F32 if u.dtype == torch.float32 else NUCLEUS_F64
+
+
+def _output(t, shape, dtype, name, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"out.{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    return t
+
+
+def sample_given(logits: torch.Tensor, temperature, top_p, uniforms, top_k=None, min_p=None, *,
+                 want_probs: bool = False, out: Optional[GivenResult] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> GivenResult:
+    """The chain of ``sample`` drawn by inverse CDF from ``uniforms`` that the
+    caller brings (``nucleus_sample_given``): row b's kept set is that of
+    ``sample``, and draw n takes the lowest kept token whose running weight
+    exceeds ``uniforms[b, n]`` of the whole.
+
+    ``logits`` [B, V] is float32, bfloat16 or float16 (rows may be strided);
+    ``uniforms`` [B, N] (N draws a row from one distribution) or [B], float32
+    or float64, in [0, 1).  ``temperature``, ``top_p``, ``top_k`` and
+    ``min_p`` are per row, as for ``sample``.  ``want_probs`` also returns
+    the kept distribution.  Launches on ``stream`` (default: the current
+    stream) and returns without synchronising."""
+    if not torch.is_tensor(logits) or logits.dtype not in _CODES:
+        raise TypeError("logits must be a float32, bfloat16 or float16 tensor")
+    _no_grad("sample_given", logits)
+    if not logits.is_cuda:
+        raise NucleusError("logits must be on the GPU: this library has no CPU path")
+    dev = logits.device
+    with _scope(dev, stream)[1]:
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        logits = _matrix(logits, "logits")
+        B, V = logits.shape
+        U, ucode = _uniforms(uniforms, ((B,), (B, None)), dev)
+        T = _vec(temperature, B, torch.float32, "temperature", dev)
+        P = _vec(top_p, B, torch.float32, "top_p", dev)
+        K = _vec(top_k, B, torch.int32, "top_k", dev)
+        MP = _vec(min_p, B, torch.float32, "min_p", dev)
+        o = out if out is not None else GivenResult(None, None, None, None)
+        res = GivenResult(_output(o.token, U.shape, torch.int32, "token", dev),
+                          _output(o.keep_count, (B,), torch.int32, "keep_count", dev),
+                          _output(o.logprob, U.shape, torch.float32, "logprob", dev),
+                          _output(o.probs, (B, V), torch.float32, "probs", dev)
+                          if want_probs or o.probs is not None else None)
+        opt = _Options()
+        opt.dtype = _CODES[logits.dtype]
+        opt.stream = s.cuda_stream
+        opt.row_stride = logits.stride(0) if B > 1 else V
+        rc = lib().nucleus_sample_given(
+            logits.data_ptr(), B, V, T.data_ptr(), P.data_ptr(), None if K is None else K.data_ptr(),
+            None if MP is None else MP.data_ptr(), U.data_ptr(), ucode, U.shape[1] if U.dim() == 2 else 1,
+            res.token.data_ptr(), res.keep_count.data_ptr(), res.logprob.data_ptr(),
+            None if res.probs is None else res.probs.data_ptr(), ctypes.byref(opt))
+    _check(rc, "nucleus_sample_given")
+    return res
+
+
+def spec_verify_given(target_probs: torch.Tensor, draft_probs: torch.Tensor, draft_token, uniforms, *,
+                      out: Optional[SpecResult] = None, stream: Optional[torch.cuda.Stream] = None) -> SpecResult:
+    """``spec_verify`` from ``uniforms`` [B, 2] that the caller brings
+    (``nucleus_spec_verify_given``): accept each row's draft token iff
+    ``uniforms[b, 0] * q < p``, else draw by inverse CDF with
+    ``uniforms[b, 1]`` from the normalised positive part of p - q."""
+    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+        if not torch.is_tensor(t) or t.dim() != 2 or t.dtype != torch.float32 or not t.is_cuda:
+            raise ValueError(f"{name} must be a float32 [B, V] tensor on the GPU")
+    if target_probs.shape != draft_probs.shape or target_probs.device != draft_probs.device:
+        raise ValueError("target_probs and draft_probs must have the same shape and device")
+    _no_grad("spec_verify_given", target_probs, draft_probs)
+    B, V = target_probs.shape
+    dev = target_probs.device
+    with _scope(dev, stream)[1]:
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        Pt, Qt = target_probs.contiguous(), draft_probs.contiguous()
+        D = _vec(draft_token, B, torch.int32, "draft_token", dev)
+        U, ucode = _uniforms(uniforms, ((B, 2),), dev)
+        o = out if out is not None else SpecResult(None, None)
+        res = SpecResult(_output(o.token, (B,), torch.int32, "token", dev),
+                         _output(o.accepted, (B,), torch.int32, "accepted", dev))
+        # A workspace of the call's own: stream-ordered when it is freed, and
+        # under graph capture the graph's.
+        ws = torch.empty(lib().nucleus_spec_given_workspace_bytes(B, V), dtype=torch.uint8, device=dev)
+        opt = _Options()
+        opt.stream = s.cuda_stream
+        opt.workspace, opt.workspace_bytes = ws.data_ptr(), ws.numel()
+        rc = lib().nucleus_spec_verify_given(Pt.data_ptr(), Qt.data_ptr(), D.data_ptr(), B, V, U.data_ptr(), ucode,
+                                             res.token.data_ptr(), res.accepted.data_ptr(), ctypes.byref(opt))
+    _check(rc, "nucleus_spec_verify_given")
+    return res
 
 
 def stream_read(buf: torch.Tensor, sink: torch.Tensor, stream: Optional[torch.cuda.Stream] = None):

@@ -21,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnucleus.so")
 LIB_STAMPS = os.path.join(HERE, "libnucleus_stamps.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("nucleus.hip", "project.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("nucleus.hip", "project.hip", "given.hip")]
 OBJDIR = os.path.join(ROOT, "_build")
 EXTRA = {}  # per-source extra hipcc flags
 

@@ -1,0 +1,929 @@
+// given.h -- the sampler's chain drawn from random numbers the caller brings:
+// temperature -> min-p -> top-k -> top-p -> renormalise, then the inverse CDF
+// in index order ("Top-p (Nucleus) Sampling, in depth", "Batched top-p with a
+// different p per request", sample_top_p; "Implement batched top-p sampling
+// with temperature", sample), N draws per row from one distribution.
+//
+//   token = lowest kept i with  sum_{j <= i, j kept} w_j  >  u sum_{j kept} w_j
+//
+// A draw is decided by where u S falls among up to V running sums, so masses
+// are carried to about 1e-13 (doubles and 45-bit integers), not to the 1e-7
+// that the race needs.
+//
+// Weights.  y = x s with s = 16 log2(e) / T: a cell a = floor(y) spans a
+// sixteenth of an octave of weight, and a token of cell a weighs
+//
+//     2^((a + 1/2)/16) * 2^(h/16),   h = y - a - 1/2 in [-1/2, 1/2),
+//
+// the second factor by its Taylor polynomial of degree 5 (|h ln2 / 16| <
+// 0.0217, so the first term left out is below 1.5e-13).  Cells do not move
+// with the row max, so one pass finds the max and histograms the row.  A
+// histogram slot sums the second factors as integers of `bits` fractional
+// bits (62 - ceil(log2 V), at most 50): exact in any order.  The window holds
+// 1024 cells (64 octaves) below the max of the first tokens loaded and 1024
+// above it; what is further down weighs less than 2^-64 of the max each and
+// is counted only.  A row whose max lies above the window takes the pass again.
+//
+// The cuts.  With the cells ranked down from the max's (rank 0), top-k or
+// min-p cut through one bottom cell rb.  The survivors' mass S lies between
+// that of the cells above rb and that with rb, so the top-p cut lies in a
+// cell of a range [r_lo, r_hi], one cell unless rb holds much mass.  One more
+// pass sums the tokens above r_lo per index segment and lists those of the
+// cells [r_lo, r_hi] and rb; the list then gives rb's exact survivors, S, the
+// crossing cell and by radix select (select.h) the exact cut level.  A row
+// with more than kGivenCap such tokens reads them from memory again wherever
+// the list would have been read.
+//
+// One workgroup per row; the draw finds its segment from the segments' sums,
+// then reads that segment alone.
+#pragma once
+
+#include "common.h"
+#include "params.h"
+#include "select.h"
+
+namespace nucleus {
+
+constexpr int kGivenThreads = 1024;
+constexpr int kGivenWaves = kGivenThreads / kWave;
+constexpr int kSlots = 2048;      // histogram window
+constexpr int kSlotsBelow = 1024; // of it, below the anchor
+constexpr int kGivenCap = 8192;   // listed tokens of undecided cells
+constexpr int kSubs = 1024;       // index segments, at most
+constexpr int kRankNone = 0x7FFFFFFF;
+constexpr int kRankZero = 1 << 15;  // a rank whose weight is 0 in double (2^-2048)
+
+struct GivenParams {
+    const void* logits;        // [B, stride]
+    int64_t B, V, stride;
+    const float* temperature;  // [B]
+    const float* top_p;        // [B]
+    const int32_t* top_k;      // [B] or null
+    const float* min_p;        // [B] or null
+    const void* uniforms;      // [B, N]
+    int64_t N;
+    int u_f64;
+    int32_t* out_token;        // [B, N]
+    int32_t* out_count;        // [B]
+    float* out_logprob;        // [B, N] or null
+    float* out_probs;          // [B, V] or null
+    int vec;                   // rows start on 16-byte boundaries
+    int bits;                  // fractional bits of in-cell weights
+};
+
+// 2^(i/16), i = 0 .. 15, correctly rounded.
+__device__ constexpr double kRoot16[16] = {
+    1.0, 1.0442737824274138, 1.0905077326652577, 1.1387886347566916, 1.189207115002721, 1.241857812073484,
+    1.2968395546510096, 1.3542555469368927, 1.4142135623730951, 1.4768261459394993, 1.5422108254079407,
+    1.6104903319492543, 1.681792830507429, 1.7562521603732995, 1.8340080864093424, 1.9152065613971474};
+
+// The row's lattice.
+struct Cells {
+    double s;     // cells per logit unit; 0 for T = +inf
+    double base;  // cell of slot 0
+};
+
+__device__ __forceinline__ Cells uniform(const Cells& c) { return Cells{uniform(c.s), uniform(c.base)}; }
+
+// Slot of a finite logit (far below the window: negative; above: >= kSlots;
+// saturated to int32) and its place h in its cell.
+__device__ __forceinline__ int slot_of(const Cells& c, float x, double& h)
+{
+#pragma clang fp contract(off)
+    const double y = (double)x * c.s;
+    const double a = floor(y);
+    h = (y - a) - 0.5;
+    return cvt_i32_sat(a - c.base);
+}
+
+// 2^(h/16) by Taylor's polynomial, |h| <= 1/2.
+__device__ __forceinline__ double in_cell(double h)
+{
+    constexpr double l = 0.69314718055994530942 / 16.0;
+    constexpr double c1 = l, c2 = l * l / 2, c3 = l * l * l / 6, c4 = l * l * l * l / 24, c5 = l * l * l * l * l / 120;
+    return fma(fma(fma(fma(fma(c5, h, c4), h, c3), h, c2), h, c1), h, 1.0);
+}
+
+// The integer q 2^bits, rounded to nearest, for q 2^bits < 2^52: adding 2^52
+// leaves it in the low bits of the double.
+__device__ __forceinline__ uint64_t fixed_point(double q, double scale)
+{
+    return (uint64_t)__double_as_longlong(fma(q, scale, 0x1p52)) - 0x4330000000000000ull;
+}
+
+// 2^(-rank/16) for 0 <= rank; root: kRoot16 in LDS.
+__device__ __forceinline__ double rank_weight(const double* root, int rank)
+{
+    const int r = min(rank, kRankZero);
+    return ldexp(root[(-r) & 15], (-r) >> 4);
+}
+
+template <int DT> struct Group;
+template <> struct Group<kF32> { static constexpr int N = 4; };
+template <> struct Group<kBF16> { static constexpr int N = 8; };
+template <> struct Group<kF16> { static constexpr int N = 8; };
+
+template <int DT>
+__device__ __forceinline__ float logit_at(const void* row, int64_t i)
+{
+    if constexpr (DT == kF32) return ((const float*)row)[i];
+    if constexpr (DT == kBF16) return bf16_to_float(((const uint16_t*)row)[i]);
+    if constexpr (DT == kF16) return (float)((const _Float16*)row)[i];
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack(u32x4 v, float (&x)[Group<DT>::N])
+{
+    if constexpr (DT == kF32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(v[j]);
+    } else if constexpr (DT == kBF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(v[j] << 16);
+            x[2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
+        }
+    } else {
+        typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+        const h8 h = __builtin_bit_cast(h8, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = (float)h[j];
+    }
+}
+
+// Group g of the row (tokens N g .. N g + N - 1) widened to fp32; -inf past
+// the row's end.
+template <int DT>
+__device__ __forceinline__ void load_group(const GivenParams& p, const void* row, uint32_t g, float (&x)[Group<DT>::N])
+{
+    constexpr int N = Group<DT>::N;
+    const int64_t i0 = (int64_t)g * N;
+    if (p.vec && i0 + N <= p.V) {
+        unpack<DT>(*((const u32x4*)row + g), x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = i0 + j < p.V ? logit_at<DT>(row, i0 + j) : -INFINITY;
+    }
+}
+
+// How a row's groups are dealt out: wave w owns the `steps` * 64 groups from
+// w * steps * 64, and its segments are runs of `sps` steps.
+struct Deal {
+    uint32_t groups;  // of the row
+    uint32_t steps;   // of 64 groups, per wave
+    uint32_t sps;     // steps per segment
+    uint32_t spw;     // segments per wave
+};
+
+template <int DT>
+__device__ __forceinline__ Deal deal_out(int64_t V)
+{
+    Deal d;
+    d.groups = (uint32_t)((V + Group<DT>::N - 1) / Group<DT>::N);
+    d.steps = (d.groups + kGivenThreads - 1) / kGivenThreads;
+    d.sps = max(8u, (d.steps + kSubs / kGivenWaves - 1) / (kSubs / kGivenWaves));
+    d.spw = (d.steps + d.sps - 1) / d.sps;
+    return d;
+}
+
+struct GivenShared {
+    uint64_t hist[kSlots];
+    uint32_t cnt[kSlots];
+    uint2 list[kGivenCap];     // key, index
+    double sub[kSubs];         // mass of each segment's surely kept tokens; then of the segments up to it (-1: empty)
+    uint64_t subc[kSubs];      // mass of its kept listed tokens, at 2^-bits
+    double pre[kSubs];         // mass of the segments before it
+    double root[16];
+    SelectShared sel;
+    uint64_t red64[kGivenWaves];
+    double redf[kGivenWaves];
+    uint32_t list_n;
+    // decided by one thread, read by all
+    double s_above, a_lo, w_bottom;
+    uint32_t n_above, n_window;
+    int r_lo, r_hi, cross;
+    uint64_t tc;
+};
+
+struct MinI { __device__ int operator()(int a, int b) const { return a < b ? a : b; } };
+struct MaxF32 { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
+
+// Exclusive prefix sum over the workgroup's threads in one fixed order;
+// `total` is the whole sum.
+__device__ __forceinline__ double block_exclusive_sum_f64(double v, double* scratch, double& total)
+{
+    const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+    double wt;
+    const double inc = wave_inclusive_sum(v, wt);
+    const double prev = wave_shift_up1(inc);
+    __syncthreads();
+    if (lane == 0) scratch[w] = wt;
+    __syncthreads();
+    double off = 0.0, all = 0.0;
+#pragma unroll
+    for (int i = 0; i < kGivenWaves; ++i) {
+        if (i == w) off = all;
+        all += scratch[i];
+    }
+    total = all;
+    return lane == 0 ? off : off + prev;
+}
+
+// Mode of a row once its max is known.
+enum : int {
+    kGivenError = 0,   // token -1
+    kGivenGreedy = 1,
+    kGivenLevel = 2,   // kept: x >= a level known at once
+    kGivenCells = 3,   // kept: by cells and the listed tokens
+};
+
+template <int DT>
+__global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
+{
+    constexpr int GN = Group<DT>::N;
+    __shared__ GivenShared sh;
+    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+    const int64_t b = blockIdx.x;
+    const size_t esz = DT == kF32 ? 4 : 2;
+    const void* row = (const char*)p.logits + (size_t)b * (size_t)p.stride * esz;
+    const Deal d = deal_out<DT>(p.V);
+    const uint32_t g_wave = (uint32_t)w * d.steps * kWave;
+    const double scale = ldexp(1.0, p.bits), inv_scale = ldexp(1.0, -p.bits);
+
+    const float T = p.temperature[b], P = p.top_p[b];
+    const int K = p.top_k ? p.top_k[b] : 0;
+    const float MP = p.min_p ? p.min_p[b] : 0.0f;
+    const bool greedy = T <= 0.0f;
+    const bool use_k = K > 0 && (int64_t)K < p.V;
+    // A histogram is needed where a cut has to be searched for.
+    const bool want_hist = !greedy && P > 0.0f && (P < 1.0f || use_k);
+
+    if (t < 16) sh.root[t] = kRoot16[t];
+    for (int i = t; i < kSubs; i += kGivenThreads) {
+        sh.sub[i] = 0.0;
+        sh.subc[i] = 0;
+    }
+    if (t == 0) sh.list_n = 0;
+
+    // ---- pass 1: max, NaN / +inf, histogram -----------------------------
+    Cells c;
+    c.s = (greedy || T == INFINITY) ? 0.0 : (16.0 * 1.4426950408889634074) / (double)T;
+    c.base = 0.0;
+    float m = -INFINITY;
+    uint64_t best = 0;      // greedy: (key, ~index) of the max
+    bool bad = false;
+    uint32_t tail = 0;      // finite tokens below the window, this thread
+    float anchor = -INFINITY;
+    {
+        // The anchor: the max of every thread's first group.
+        float x[GN];
+        const uint32_t g = g_wave + lane;
+        if (g < d.groups && want_hist) {
+            load_group<DT>(p, row, g, x);
+#pragma unroll
+            for (int j = 0; j < GN; ++j) anchor = fmaxf(anchor, x[j]);
+        }
+        __syncthreads();
+        if (want_hist) anchor = block_reduce<kGivenThreads>(anchor, MaxF32(), (float*)sh.redf);
+    }
+    // At most two attempts: the second is anchored at the row's own max.
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        const bool hist = want_hist && anchor > -INFINITY && anchor < INFINITY;
+        if (hist) {
+            c.base = floor((double)anchor * c.s) - kSlotsBelow;
+            for (int i = t; i < kSlots; i += kGivenThreads) {
+                sh.hist[i] = 0;
+                sh.cnt[i] = 0;
+            }
+            __syncthreads();
+        }
+        c = uniform(c);
+        tail = 0;
+        bool over = false;
+        for (uint32_t i = 0; i < d.steps; ++i) {
+            const uint32_t g = g_wave + i * kWave + lane;
+            if (g >= d.groups) break;
+            float x[GN];
+            load_group<DT>(p, row, g, x);
+#pragma unroll
+            for (int j = 0; j < GN; ++j) {
+                bad |= !(x[j] < INFINITY);  // NaN or +inf
+                m = fmaxf(m, x[j]);
+                if (greedy) {
+                    const uint64_t pk = ((uint64_t)order_key(x[j]) << 32) | (uint32_t)~(uint32_t)(g * GN + j);
+                    best = pk > best ? pk : best;
+                }
+                if (hist && x[j] > -INFINITY) {
+                    double h;
+                    const int sl = slot_of(c, x[j], h);
+                    if ((uint32_t)sl < (uint32_t)kSlots) {
+                        atomicAdd((unsigned long long*)&sh.hist[sl], (unsigned long long)fixed_point(in_cell(h), scale));
+                        if (use_k) atomicAdd(&sh.cnt[sl], 1u);
+                    } else if (sl < 0) {
+                        ++tail;
+                    } else {
+                        over = true;
+                    }
+                }
+            }
+        }
+        m = block_reduce<kGivenThreads>(m, MaxF32(), (float*)sh.redf);
+        const int again = block_reduce<kGivenThreads>((int)over, OrI32(), (int*)sh.redf);
+        if (!want_hist || (hist && !again) || !(m > -INFINITY && m < INFINITY)) break;
+        anchor = m;
+        __syncthreads();
+    }
+    bad = block_reduce<kGivenThreads>((int)bad, OrI32(), (int*)sh.redf) != 0;
+    m = uniform(m);
+
+    int mode = kGivenCells;
+    float level = -INFINITY;  // kGivenLevel: kept iff x >= level (and finite)
+    if (bad || !(m > -INFINITY) || isnan(T) || isnan(P) || isnan(MP)) {
+        mode = kGivenError;
+    } else if (greedy) {
+        mode = kGivenGreedy;
+    }
+    // min-p: w_i >= min_p w_max  <=>  x_i >= m + T ln(min_p), rounded up.
+    float tmp = -INFINITY;
+    if (mode == kGivenCells) {
+        const float mpc = MP > 1.0f ? 1.0f : MP;
+        if (mpc > 0.0f && T != INFINITY) {
+            const double td = (double)m + (double)T * log((double)mpc);
+            float tf = (float)td;
+            if ((double)tf < td) tf = nextafterf(tf, INFINITY);
+            tmp = uniform(tf);
+        }
+        if (P <= 0.0f) {
+            mode = kGivenLevel;
+            level = m;
+        } else if (!want_hist) {
+            mode = kGivenLevel;
+            level = tmp;
+        }
+    }
+
+    if (mode == kGivenError || mode == kGivenGreedy) {
+        int token = -1;
+        if (mode == kGivenGreedy) {
+            best = block_reduce<kGivenThreads>(best, MaxU64(), sh.red64);
+            token = (int)~(uint32_t)best;
+        }
+        if (t == 0) p.out_count[b] = mode == kGivenGreedy ? 1 : 0;
+        for (int64_t n = t; n < p.N; n += kGivenThreads) {
+            p.out_token[b * p.N + n] = token;
+            if (p.out_logprob) p.out_logprob[b * p.N + n] = mode == kGivenGreedy ? 0.0f : __uint_as_float(0x7FC00000u);
+        }
+        if (p.out_probs)
+            for (int64_t i = t; i < p.V; i += kGivenThreads) p.out_probs[b * p.V + i] = i == token ? 1.0f : 0.0f;
+        return;
+    }
+
+    // ---- the cells of the cuts -------------------------------------------
+    double hm;  // place of the max in its cell
+    if (mode == kGivenLevel) c.base = floor((double)m * c.s) - kSlotsBelow;
+    c = uniform(c);
+    const int top = slot_of(c, m, hm);  // slot of rank 0
+    int rb = kRankNone;                 // bottom cell
+    int r_lo = 0, r_hi = -1;
+    const bool cut_p = P < 1.0f;
+    if (mode == kGivenCells) {
+        constexpr int PER = kSlots / kGivenThreads;
+        double wt[PER], run = 0.0;
+        uint32_t ct[PER], crun = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = PER * t + i, sl = top - r;
+            wt[i] = sl >= 0 && sh.hist[sl] ? rank_weight(sh.root, r) * ((double)sh.hist[sl] * inv_scale) : 0.0;
+            ct[i] = sl >= 0 && use_k ? sh.cnt[sl] : 0u;
+            run += wt[i];
+            crun += ct[i];
+        }
+        double total;
+        const double before = block_exclusive_sum_f64(run, sh.redf, total);
+        const uint32_t cbefore = (uint32_t)block_exclusive_sum<kGivenThreads>(crun, sh.red64);
+        int rk = kRankNone;
+        if (use_k) {
+            uint32_t cc = cbefore;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                cc += ct[i];
+                if (rk == kRankNone && cc >= (uint32_t)K && ct[i]) rk = PER * t + i;
+            }
+            rk = block_reduce<kGivenThreads>(rk, MinI(), (int*)sh.redf);
+        }
+        double ht;
+        // min-p's threshold is at or below the max, and may lie below the window
+        const int64_t st = tmp > -INFINITY ? (int64_t)slot_of(c, tmp, ht) : (int64_t)-1;
+        const int rt = tmp > -INFINITY ? (int)min((int64_t)top - st, (int64_t)top + 1) : kRankNone;
+        rb = min(rk, rt);
+        if (cut_p && rb > top) rb = kRankNone;  // below the window: the top-p cut is above it
+        const uint32_t tails = (uint32_t)block_reduce<kGivenThreads>((uint64_t)tail, SumU64(), sh.red64);
+        if (t == kGivenThreads - 1) {
+            sh.n_window = cbefore + crun;
+            sh.n_above = cbefore + crun;
+            sh.s_above = total;
+            sh.w_bottom = 0.0;
+        }
+        __syncthreads();
+        if (rb <= top) {
+            const int o = rb - PER * t;
+            if (o >= 0 && o < PER) {
+                double ab = before;
+                uint32_t ca = cbefore;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (i < o) {
+                        ab += wt[i];
+                        ca += ct[i];
+                    }
+                double wb = 0.0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (i == o) wb = wt[i];
+                sh.s_above = ab;
+                sh.n_above = ca;
+                sh.w_bottom = wb;
+            }
+        } else if (rb == kRankNone && use_k && !cut_p && (uint64_t)sh.n_window + tails > (uint64_t)K) {
+            rb = top + 1;  // top-k cuts among the tokens below the window: they are listed as one cell
+        }
+        __syncthreads();
+        if (cut_p) {
+            const double lo = (double)P * sh.s_above, hi = (double)P * (sh.s_above + sh.w_bottom);
+            int first_lo = kRankNone, first_hi = kRankNone, last = -1;
+            double ab = before;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int r = PER * t + i;
+                if (wt[i] > 0.0 && r < rb) {
+                    last = r;
+                    if (first_lo == kRankNone && ab + wt[i] >= lo) first_lo = r;
+                    if (first_hi == kRankNone && ab + wt[i] >= hi) first_hi = r;
+                }
+                ab += wt[i];
+            }
+            first_lo = block_reduce<kGivenThreads>(first_lo, MinI(), (int*)sh.redf);
+            first_hi = block_reduce<kGivenThreads>(first_hi, MinI(), (int*)sh.redf);
+            last = block_reduce<kGivenThreads>(last, MaxI32(), (int*)sh.redf);
+            const int end = rb <= top ? rb : last;  // where rounding leaves none above
+            r_lo = min(first_lo, end);
+            r_hi = min(first_hi, end);
+            const int o = r_lo - PER * t;
+            if (o >= 0 && o < PER) {
+                double a = before;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (i < o) a += wt[i];
+                sh.a_lo = a;
+            }
+        } else {
+            r_lo = rb;  // every cell above the bottom one is kept
+            r_hi = rb;
+        }
+        r_lo = uniform(r_lo);
+        r_hi = uniform(r_hi);
+        rb = uniform(rb);
+    }
+
+    // Rank of a finite token's cell; all cells below the window are one.
+    auto rank_of = [&](float x, double& h) {
+        const int sl = slot_of(c, x, h);
+        return sl >= 0 ? top - sl : top + 1;
+    };
+    // The rank that its weight goes by (no limit at the window's end).
+    auto weight_of = [&](float x) {
+#pragma clang fp contract(off)
+        double h;
+        const int sl = slot_of(c, x, h);
+        const int64_t r = (int64_t)top - sl;
+        return rank_weight(sh.root, (int)min(r, (int64_t)kRankZero)) * in_cell(h);
+    };
+
+    // ---- pass 2: masses of the surely kept, list of the undecided -----------
+    uint32_t count = 0;
+    {
+        double acc = 0.0;
+        for (uint32_t i = 0; i < d.steps; ++i) {
+            const uint32_t g = g_wave + i * kWave + lane;
+            if (g < d.groups) {
+                float x[GN];
+                load_group<DT>(p, row, g, x);
+#pragma unroll
+                for (int j = 0; j < GN; ++j) {
+                    if (!(x[j] > -INFINITY)) continue;
+                    if (mode == kGivenLevel) {
+                        if (x[j] >= level) {
+                            acc += weight_of(x[j]);
+                            ++count;
+                        }
+                    } else {
+                        double h;
+                        const int r = rank_of(x[j], h);
+                        if (r < r_lo) {
+                            acc += weight_of(x[j]);
+                            ++count;
+                        } else if (r <= r_hi || r == rb) {
+                            const uint32_t at = atomicAdd(&sh.list_n, 1u);
+                            if (at < kGivenCap) sh.list[at] = make_uint2(order_key(x[j]), g * GN + j);
+                        }
+                    }
+                }
+            }
+            if ((i + 1) % d.sps == 0 || i + 1 == d.steps) {
+                const double sum = wave_reduce(acc, [](double a, double e) { return a + e; });
+                if (lane == 0) sh.sub[w * d.spw + i / d.sps] = sum;
+                acc = 0.0;
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- the exact cut level ---------------------------------------------
+    uint32_t cut = mode == kGivenLevel ? (level > -INFINITY ? order_key(level) : order_key(-3.402823466e38f)) : 0u;
+    if (mode == kGivenCells) {
+        const uint32_t ln = sh.list_n;
+        const bool listed = ln <= kGivenCap;
+        // Every undecided token (key, index), from the list or from memory.
+        auto undecided = [&](auto fn) {
+            if (listed) {
+                for (uint32_t i = t; i < ln; i += kGivenThreads) {
+                    const uint2 e = sh.list[i];
+                    double h;
+                    const int r = rank_of(key_value(e.x), h);
+                    fn(e.x, e.y, r, h);
+                }
+            } else {
+                for (uint32_t i = 0; i < d.steps; ++i) {
+                    const uint32_t g = g_wave + i * kWave + lane;
+                    if (g >= d.groups) break;
+                    float x[GN];
+                    load_group<DT>(p, row, g, x);
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) {
+                        if (!(x[j] > -INFINITY)) continue;
+                        double h;
+                        const int r = rank_of(x[j], h);
+                        if (r >= r_lo && (r <= r_hi || r == rb)) fn(order_key(x[j]), g * GN + j, r, h);
+                    }
+                }
+            }
+        };
+        // The bottom cell: min-p's threshold, then the k-th largest.
+        uint32_t bottom = tmp > -INFINITY ? order_key(tmp) : order_key(-3.402823466e38f);
+        double s_bottom = 0.0;
+        if (rb != kRankNone) {
+            const uint32_t from_minp = bottom;
+            if (use_k && sh.n_above < (uint32_t)K) {
+                const uint64_t need = (uint64_t)K - sh.n_above;
+                const SelectResult r = select_level<kGivenThreads>(
+                    [&](auto fn) {
+                        undecided([&](uint32_t key, uint32_t, int rank, double) {
+                            if (rank == rb && key >= from_minp) fn(key, (uint64_t)1);
+                        });
+                    },
+                    [&](uint64_t) { return need; }, sh.sel);
+                if (r.total) bottom = max(bottom, r.level);
+                __syncthreads();
+            }
+            if (rb <= top) {
+                uint64_t fx = 0;
+                undecided([&](uint32_t key, uint32_t, int rank, double h) {
+                    if (rank == rb && key >= bottom) fx += fixed_point(in_cell(h), scale);
+                });
+                fx = block_reduce<kGivenThreads>(fx, SumU64(), sh.red64);
+                s_bottom = rank_weight(sh.root, rb) * ((double)fx * inv_scale);
+            }
+        }
+        cut = bottom;
+        if (cut_p) {
+            if (t == 0) {
+                // The crossing cell: the first whose running mass reaches p S.
+                const double thr = (double)P * (sh.s_above + s_bottom);
+                double a = sh.a_lo, at = sh.a_lo;
+                int r = r_lo, found = r_lo;
+                for (; r <= r_hi; ++r) {
+                    const uint64_t hr = sh.hist[top - r];
+                    const double wr = r == rb ? s_bottom : rank_weight(sh.root, r) * ((double)hr * inv_scale);
+                    if (wr > 0.0) {
+                        found = r;
+                        at = a;
+                        if (a + wr >= thr) break;
+                    }
+                    a += wr;
+                }
+                const double q = (thr - at) / (rank_weight(sh.root, found) * inv_scale);
+                sh.cross = found;
+                sh.tc = !(q > 1.0) ? 1 : (q < 1.8e19 ? (uint64_t)ceil(q) : ~0ull);
+            }
+            __syncthreads();
+            const int cp = uniform(sh.cross);
+            const uint64_t tc = sh.tc;
+            const SelectResult r = select_level<kGivenThreads>(
+                [&](auto fn) {
+                    undecided([&](uint32_t key, uint32_t, int rank, double h) {
+                        if (rank == cp && key >= bottom) fn(key, fixed_point(in_cell(h), scale));
+                    });
+                },
+                [&](uint64_t) { return tc; }, sh.sel);
+            cut = max(bottom, r.level);
+        }
+        // The kept among them, added to their segments.
+        undecided([&](uint32_t key, uint32_t idx, int, double) {
+            if (key >= cut) {
+                const uint32_t g = idx / GN, own = g / (d.steps * kWave), step = (g - own * d.steps * kWave) / kWave;
+                atomicAdd((unsigned long long*)&sh.subc[own * d.spw + step / d.sps],
+                          (unsigned long long)fixed_point(weight_of(key_value(key)), scale));
+                ++count;
+            }
+        });
+        __syncthreads();
+    }
+    const float low = key_value(cut);  // kept: finite and x >= low
+
+    // ---- the draws ---------------------------------------------------------
+    count = (uint32_t)block_reduce<kGivenThreads>((uint64_t)count, SumU64(), sh.red64);
+    const uint32_t subs = d.spw * kGivenWaves;
+    const double mine = t < (int)subs ? sh.sub[t] + (double)sh.subc[t] * inv_scale : 0.0;
+    double S;
+    const double prefix = block_exclusive_sum_f64(mine, sh.redf, S);
+    __syncthreads();
+    if (t < (int)subs) {
+        sh.sub[t] = mine > 0.0 ? prefix + mine : -1.0;
+        sh.pre[t] = prefix;
+    }
+    __syncthreads();
+    if (t == 0) p.out_count[b] = (int32_t)count;
+    // ln of the kept mass measured from the max itself.
+    const double ln_mass = log(S) - hm * (0.69314718055994530942 / 16.0);
+    for (int64_t n = w; n < p.N; n += kGivenWaves) {
+        const double u = p.u_f64 ? ((const double*)p.uniforms)[b * p.N + n] : (double)((const float*)p.uniforms)[b * p.N + n];
+        int token = -1;
+        if (u == u) {
+            const double at = (u < 0.0 ? 0.0 : (u > 1.0 ? 1.0 : u)) * S;
+            // The first segment whose running sum exceeds `at`; past the end, the last with mass.
+            uint32_t lo = 0;
+            bool found = false;
+            for (uint32_t i = 0; i < subs && !found; i += kWave) {
+                const double v = i + lane < subs ? sh.sub[i + lane] : -1.0;
+                const uint64_t over = __ballot(v > at), any = __ballot(v >= 0.0);
+                if (over) {
+                    lo = i + (uint32_t)__builtin_ctzll(over);
+                    found = true;
+                } else if (any) {
+                    lo = i + 63u - (uint32_t)__builtin_clzll(any);
+                }
+            }
+            double run = sh.pre[lo];
+            const uint32_t own = lo / d.spw, s0 = (lo - own * d.spw) * d.sps;
+            int last = -1;
+            for (uint32_t i = s0; i < min(s0 + d.sps, d.steps); ++i) {
+                const uint32_t g = (own * d.steps + i) * kWave + lane;
+                double wg[GN], sum = 0.0;
+                int mine_last = -1;
+                float x[GN];
+                if (g < d.groups) {
+                    load_group<DT>(p, row, g, x);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) x[j] = -INFINITY;
+                }
+#pragma unroll
+                for (int j = 0; j < GN; ++j) {
+                    const bool kept = x[j] > -INFINITY && x[j] >= low;
+                    wg[j] = kept ? weight_of(x[j]) : 0.0;
+                    sum += wg[j];
+                    if (wg[j] > 0.0) mine_last = (int)(g * GN + j);
+                }
+                double all;
+                const double inc = wave_inclusive_sum(sum, all);
+                const double prev = wave_shift_up1(inc);
+                const uint64_t hit = __ballot(run + inc > at);
+                if (hit) {
+                    const int L = (int)__builtin_ctzll(hit);
+                    double a = run + (lane ? prev : 0.0);
+                    int tok = -1;
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) {
+                        a += wg[j];
+                        if (tok < 0 && a > at && wg[j] > 0.0) tok = (int)(g * GN + j);
+                    }
+                    if (tok < 0) tok = mine_last;
+                    token = __builtin_amdgcn_readlane(tok, L);
+                    if (token >= 0) break;
+                }
+                run += all;
+                last = max(last, wave_reduce(mine_last, MaxI32()));
+            }
+            if (token < 0) token = last;
+        }
+        if (lane == 0) {
+            p.out_token[b * p.N + n] = token;
+            if (p.out_logprob) {
+                float lp = __uint_as_float(0x7FC00000u);
+                if (token >= 0)
+                    lp = (float)(((double)logit_at<DT>(row, token) - (double)m) / (double)T - ln_mass);
+                p.out_logprob[b * p.N + n] = lp;
+            }
+        }
+    }
+
+    // ---- the distribution ---------------------------------------------------
+    if (p.out_probs) {
+        const double inv = 1.0 / S;
+        float* out = p.out_probs + b * p.V;
+        const bool vec = p.V % 4 == 0 && (uintptr_t)p.out_probs % 16 == 0;
+        for (uint32_t g = t; g < d.groups; g += kGivenThreads) {
+            float x[GN], q[GN];
+            load_group<DT>(p, row, g, x);
+#pragma unroll
+            for (int j = 0; j < GN; ++j)
+                q[j] = x[j] > -INFINITY && x[j] >= low ? (float)(weight_of(x[j]) * inv) : 0.0f;
+            const int64_t i0 = (int64_t)g * GN;
+            if (vec && i0 + GN <= p.V) {
+#pragma unroll
+                for (int j = 0; j < GN; j += 4) *(f32x4*)(out + i0 + j) = f32x4{q[j], q[j + 1], q[j + 2], q[j + 3]};
+            } else {
+#pragma unroll
+                for (int j = 0; j < GN; ++j)
+                    if (i0 + j < p.V) out[i0 + j] = q[j];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Speculative acceptance from given uniforms: accept d iff u0 q(d) < p(d),
+// else the inverse CDF with u1 over r_i = max(p_i - q_i, 0) in index order.
+//
+// Two launches, as in spec.h: a workgroup per 8192-token chunk of every row
+// sums r over the chunks of rejected rows in doubles (in a fixed order); then
+// a workgroup per row finds the chunk and reads that chunk again.
+// ---------------------------------------------------------------------------
+constexpr int kPickThreads = 256;
+constexpr int kPickWaves = kPickThreads / kWave;
+constexpr int kPickSteps = 8;                              // of 64 groups of 4 tokens, per wave
+constexpr int kPickChunk = kPickThreads * kPickSteps * 4;  // 8192 tokens
+
+struct PickParams {
+    const float* target;         // [B, V]: p
+    const float* draft;          // [B, V]: q
+    const int32_t* draft_token;  // [B]
+    const void* uniforms;        // [B, 2]
+    int u_f64;
+    int64_t B, V;
+    int32_t* out_token;     // [B]
+    int32_t* out_accepted;  // [B] or null
+    double* part;           // [B, C] chunk sums (workspace)
+    int C;
+    int vec;                // rows 16-byte aligned
+};
+
+// 1 accepted, 0 rejected, -1 a draft token out of range or u0 not a number.
+__device__ __forceinline__ int pick_verdict(const PickParams& p, int64_t b)
+{
+    const int32_t d = p.draft_token[b];
+    const double u = p.u_f64 ? ((const double*)p.uniforms)[2 * b] : (double)((const float*)p.uniforms)[2 * b];
+    if (d < 0 || d >= p.V || !(u == u)) return -1;
+    return u * (double)p.draft[b * p.V + d] < (double)p.target[b * p.V + d] ? 1 : 0;
+}
+
+// max(p - q, 0) of step k's group of this lane in chunk c (0 for NaN and past
+// the row's end).
+__device__ __forceinline__ void pick_load(const PickParams& p, int64_t b, int c, int k, double (&r)[4])
+{
+    const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+    const int64_t i0 = (int64_t)c * kPickChunk + (int64_t)((w * kPickSteps + k) * kWave + lane) * 4;
+    const float *P = p.target + b * p.V, *Q = p.draft + b * p.V;
+    float a[4], e[4];
+    if (p.vec && i0 + 4 <= p.V) {
+        const f32x4 va = *(const f32x4*)(P + i0), ve = *(const f32x4*)(Q + i0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[j] = va[j];
+            e[j] = ve[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[j] = i0 + j < p.V ? P[i0 + j] : 0.0f;
+            e[j] = i0 + j < p.V ? Q[i0 + j] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const double v = (double)a[j] - (double)e[j];
+        r[j] = v > 0.0 ? v : 0.0;
+    }
+}
+
+struct SumF64 { __device__ double operator()(double a, double b) const { return a + b; } };
+
+__global__ __launch_bounds__(kPickThreads) void pick_chunk_kernel(PickParams p)
+{
+    __shared__ double red[kPickWaves];
+    const int64_t b = blockIdx.x % (uint32_t)p.B;
+    const int c = (int)(blockIdx.x / (uint32_t)p.B);
+    if (pick_verdict(p, b) != 0) return;  // uniform; nothing reads the slot
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < kPickSteps; ++k) {
+        double r[4];
+        pick_load(p, b, c, k, r);
+        sum += (r[0] + r[1]) + (r[2] + r[3]);
+    }
+    sum = block_reduce<kPickThreads>(sum, SumF64(), red);
+    if (threadIdx.x == 0) p.part[b * p.C + c] = sum;
+}
+
+__global__ __launch_bounds__(kPickThreads) void pick_finish_kernel(PickParams p)
+{
+    __shared__ double wsum[kPickWaves];
+    __shared__ int wlast[kPickWaves], found[kPickWaves];
+    const int64_t b = blockIdx.x;
+    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+    const int verdict = pick_verdict(p, b);
+    if (verdict != 0) {
+        if (t == 0) {
+            p.out_token[b] = verdict > 0 ? p.draft_token[b] : -1;
+            if (p.out_accepted) p.out_accepted[b] = verdict > 0 ? 1 : 0;
+        }
+        return;
+    }
+    // Every wave finds the chunk for itself, in the same way.
+    const double* part = p.part + b * p.C;
+    double S = 0.0;
+    for (int i = 0; i < p.C; i += kWave) {
+        double all;
+        wave_inclusive_sum(i + lane < p.C ? part[i + lane] : 0.0, all);
+        S += all;
+    }
+    const double u = p.u_f64 ? ((const double*)p.uniforms)[2 * b + 1] : (double)((const float*)p.uniforms)[2 * b + 1];
+    int token = -1;
+    if (S > 0.0 && S < (double)INFINITY && u == u) {
+        const double at = (u < 0.0 ? 0.0 : (u > 1.0 ? 1.0 : u)) * S;
+        int chunk = 0;
+        double run = 0.0, before = 0.0;
+        for (int i = 0; i < p.C; i += kWave) {
+            const double v = i + lane < p.C ? part[i + lane] : 0.0;
+            double all;
+            const double inc = wave_inclusive_sum(v, all);
+            const double prev = wave_shift_up1(inc);
+            const uint64_t mass = __ballot(v > 0.0), over = __ballot(v > 0.0 && run + inc > at);
+            if (over | mass) {  // the first that exceeds `at`, or so far the last with mass
+                const int L = over ? (int)__builtin_ctzll(over) : 63 - (int)__builtin_clzll(mass);
+                chunk = i + L;
+                before = run + lane_value(prev, L);
+            }
+            if (over) break;
+            run += all;
+        }
+        double r[kPickSteps][4], sum = 0.0;
+#pragma unroll
+        for (int k = 0; k < kPickSteps; ++k) pick_load(p, b, chunk, k, r[k]);
+#pragma unroll
+        for (int k = 0; k < kPickSteps; ++k) sum += (r[k][0] + r[k][1]) + (r[k][2] + r[k][3]);
+        sum = wave_reduce(sum, SumF64());
+        if (lane == 0) wsum[w] = sum;
+        __syncthreads();
+        double a0 = before;
+        for (int i = 0; i < w; ++i) a0 += wsum[i];
+        int hit = -1, last = -1;
+#pragma unroll
+        for (int k = 0; k < kPickSteps; ++k) {
+            const int i0 = (int)((uint32_t)chunk * kPickChunk + (uint32_t)((w * kPickSteps + k) * kWave + lane) * 4u);
+            double all;
+            const double own = (r[k][0] + r[k][1]) + (r[k][2] + r[k][3]);
+            const double inc = wave_inclusive_sum(own, all);
+            const double prev = wave_shift_up1(inc);
+            double a = a0 + (lane ? prev : 0.0);
+            int tok = -1, end = -1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                a += r[k][j];
+                if (r[k][j] > 0.0) {
+                    end = i0 + j;
+                    if (tok < 0 && a > at) tok = i0 + j;
+                }
+            }
+            const uint64_t hits = __ballot(tok >= 0), ends = __ballot(end >= 0);
+            if (hit < 0 && hits) hit = __builtin_amdgcn_readlane(tok, (int)__builtin_ctzll(hits));
+            if (ends) last = __builtin_amdgcn_readlane(end, 63 - (int)__builtin_clzll(ends));
+            a0 += all;
+        }
+        if (lane == 0) {
+            found[w] = hit;
+            wlast[w] = last;
+        }
+        __syncthreads();
+        for (int i = kPickWaves - 1; i >= 0; --i)
+            if (wlast[i] >= 0 && token < 0) token = wlast[i];
+        for (int i = kPickWaves - 1; i >= 0; --i)
+            if (found[i] >= 0) token = found[i];
+    }
+    if (t == 0) {
+        p.out_token[b] = token;
+        if (p.out_accepted) p.out_accepted[b] = 0;
+    }
+}
+
+}  // namespace nucleus

@@ -1,0 +1,126 @@
+// given.hip -- the entry points that draw from random numbers the caller
+// brings: nucleus_sample_given and nucleus_spec_verify_given (declared in
+// include/nucleus.h).
+#include <hip/hip_runtime.h>
+
+#include "nucleus.h"
+#include "given.h"
+#include "host.h"
+
+using namespace nucleus;
+
+namespace {
+
+// Options that only other entry points take.
+bool other_options(const nucleus_options* o)
+{
+    return o->flags || o->seeds || o->out_logprobs || o->out_min_kept_logit || o->history || o->history_len ||
+           o->repetition_penalty || o->frequency_penalty || o->presence_penalty || o->allowed_mask ||
+           o->split_give_up_row;
+}
+
+size_t uniform_bytes(int32_t dtype) { return dtype == NUCLEUS_F64 ? 8 : 4; }
+
+}  // namespace
+
+extern "C" int nucleus_sample_given(const void* logits, int64_t B, int64_t V, const float* temperature,
+                                    const float* top_p, const int32_t* top_k, const float* min_p, const void* uniforms,
+                                    int32_t uniform_dtype, int64_t N, int32_t* out_token, int32_t* out_keep_count,
+                                    float* out_token_logprob, float* out_probs, const nucleus_options* opt)
+{
+    const nucleus_options none = {};
+    const nucleus_options& o = opt ? *opt : none;
+    const int64_t most = int64_t(1) << 31;
+    const int64_t stride = o.row_stride ? o.row_stride : V;
+    if (B < 0 || B >= most || V < 1 || V >= most || N < 1 || N >= most || stride < V) return NUCLEUS_EINVAL;
+    if (o.dtype != NUCLEUS_F32 && o.dtype != NUCLEUS_BF16 && o.dtype != NUCLEUS_F16) return NUCLEUS_EINVAL;
+    if (uniform_dtype != NUCLEUS_F32 && uniform_dtype != NUCLEUS_F64) return NUCLEUS_EINVAL;
+    if (other_options(&o)) return NUCLEUS_EINVAL;
+    if (B == 0) return NUCLEUS_OK;
+    if (!logits || !temperature || !top_p || !uniforms || !out_token || !out_keep_count) return NUCLEUS_EINVAL;
+    const size_t esz = o.dtype == NUCLEUS_F32 ? 4 : 2;
+    if ((uintptr_t)logits % esz || !aligned(temperature) || !aligned(top_p) || !aligned(top_k) || !aligned(min_p) ||
+        (uintptr_t)uniforms % uniform_bytes(uniform_dtype) || !aligned(out_token) || !aligned(out_keep_count) ||
+        !aligned(out_token_logprob) || !aligned(out_probs))
+        return NUCLEUS_EINVAL;
+    const int dev_rc = check_device();
+    if (dev_rc != NUCLEUS_OK) return dev_rc;
+
+    GivenParams p = {};
+    p.logits = logits;
+    p.B = B;
+    p.V = V;
+    p.stride = stride;
+    p.temperature = temperature;
+    p.top_p = top_p;
+    p.top_k = top_k;
+    p.min_p = min_p;
+    p.uniforms = uniforms;
+    p.N = N;
+    p.u_f64 = uniform_dtype == NUCLEUS_F64;
+    p.out_token = out_token;
+    p.out_count = out_keep_count;
+    p.out_logprob = out_token_logprob;
+    p.out_probs = out_probs;
+    p.vec = (uintptr_t)logits % 16 == 0 && ((size_t)stride * esz) % 16 == 0;
+    int log2v = 0;
+    while ((int64_t(1) << log2v) < V) ++log2v;
+    p.bits = 62 - log2v < 50 ? 62 - log2v : 50;
+    hipStream_t s = (hipStream_t)o.stream;
+    const dim3 grid((unsigned)B), block(kGivenThreads);
+    if (o.dtype == NUCLEUS_F32)
+        hipLaunchKernelGGL(given_row_kernel<kF32>, grid, block, 0, s, p);
+    else if (o.dtype == NUCLEUS_BF16)
+        hipLaunchKernelGGL(given_row_kernel<kBF16>, grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL(given_row_kernel<kF16>, grid, block, 0, s, p);
+    return hipGetLastError() == hipSuccess ? NUCLEUS_OK : NUCLEUS_ELAUNCH;
+}
+
+extern "C" size_t nucleus_spec_given_workspace_bytes(int64_t B, int64_t V)
+{
+    if (B < 0 || B >= (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31)) return 0;
+    return ((size_t)B * (size_t)((V + kPickChunk - 1) / kPickChunk) * 8 + 255) / 256 * 256;
+}
+
+extern "C" int nucleus_spec_verify_given(const float* target_probs, const float* draft_probs,
+                                         const int32_t* draft_token, int64_t B, int64_t V, const void* uniforms,
+                                         int32_t uniform_dtype, int32_t* out_token, int32_t* out_accepted,
+                                         const nucleus_options* opt)
+{
+    const int64_t most = int64_t(1) << 31;
+    if (B < 0 || B >= most || V < 1 || V >= most) return NUCLEUS_EINVAL;
+    if (uniform_dtype != NUCLEUS_F32 && uniform_dtype != NUCLEUS_F64) return NUCLEUS_EINVAL;
+    if (opt && (other_options(opt) || opt->dtype != NUCLEUS_F32 || (opt->row_stride && opt->row_stride != V)))
+        return NUCLEUS_EINVAL;
+    if (B == 0) return NUCLEUS_OK;
+    if (!target_probs || !draft_probs || !draft_token || !uniforms || !out_token) return NUCLEUS_EINVAL;
+    if (!aligned(target_probs) || !aligned(draft_probs) || !aligned(draft_token) ||
+        (uintptr_t)uniforms % uniform_bytes(uniform_dtype) || !aligned(out_token) || !aligned(out_accepted))
+        return NUCLEUS_EINVAL;
+    const int64_t C = (V + kPickChunk - 1) / kPickChunk;
+    if (B * C >= most) return NUCLEUS_EINVAL;
+    if (!opt || !opt->workspace || opt->workspace_bytes < nucleus_spec_given_workspace_bytes(B, V) ||
+        (uintptr_t)opt->workspace % 256)
+        return NUCLEUS_EWORKSPACE;
+    const int dev_rc = check_device();
+    if (dev_rc != NUCLEUS_OK) return dev_rc;
+
+    PickParams p = {};
+    p.target = target_probs;
+    p.draft = draft_probs;
+    p.draft_token = draft_token;
+    p.uniforms = uniforms;
+    p.u_f64 = uniform_dtype == NUCLEUS_F64;
+    p.B = B;
+    p.V = V;
+    p.out_token = out_token;
+    p.out_accepted = out_accepted;
+    p.part = (double*)opt->workspace;
+    p.C = (int)C;
+    p.vec = V % 4 == 0 && (uintptr_t)target_probs % 16 == 0 && (uintptr_t)draft_probs % 16 == 0;
+    hipStream_t s = (hipStream_t)opt->stream;
+    hipLaunchKernelGGL(pick_chunk_kernel, dim3((unsigned)(B * C)), dim3(kPickThreads), 0, s, p);
+    hipLaunchKernelGGL(pick_finish_kernel, dim3((unsigned)B), dim3(kPickThreads), 0, s, p);
+    return hipGetLastError() == hipSuccess ? NUCLEUS_OK : NUCLEUS_ELAUNCH;
+}
