@@ -202,4 +202,252 @@ __global__ __launch_bounds__(kAnyThreads) void project_any_kernel(ProjectParams 
         project_store<DT>(p, m0 + 16 * u + (lane & 15), n0 + 16 * w + 4 * (lane >> 4), acc[u]);
 }
 
+// ---------------------------------------------------------------------------
+// Many rows of hidden: a workgroup of WN x WM waves makes a BN (n) x BM (m)
+// tile, 128 bytes of k at a step.  Both sides' pieces go from memory straight
+// into LDS (16 bytes a lane, no registers), STAGES deep: while step s is
+// multiplied the loads of steps s + 1 .. s + STAGES - 1 are in flight, and a
+// step costs one barrier.
+//
+// LDS holds 128-byte rows (eight chunks); chunk x of row r lies at place
+// x ^ ((r / 2) % 8), so that the sixteen rows that a quarter wave reads at
+// one x fall on sixteen different 16-byte banks groups.  The loads write LDS
+// in lane order, so the permutation is made on the address a lane reads from.
+//
+// Workgroups go to the eight XCDs in turn; each XCD is given a run of
+// neighbouring tiles, so that its L2 holds the rows they share.
+// ---------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) char lds_char;
+
+// 64 lanes x 16 bytes from rsrc + soff + voff (0 where voff is out of range)
+// to LDS bytes `to` .. `to` + 1023, in lane order.  Not tracked by the
+// compiler: wait_loads() below waits for it.
+__device__ __forceinline__ void load_to_lds(uint32_t to, u32x4 rsrc, uint32_t voff, uint32_t soff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(to), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory");
+}
+
+// All but the wave's last N loads have arrived, its LDS reads have returned,
+// and every wave of the workgroup has come here.
+template <int N>
+__device__ __forceinline__ void wait_loads_and_meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+// Buffer descriptor of `bytes` bytes at p (wave-uniform).
+__device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes)
+{
+    const uint64_t a = (uint64_t)p;
+    return u32x4{uniform((uint32_t)a), uniform((uint32_t)(a >> 32)) & 0xFFFFu, uniform(bytes), 0x00020000u};
+}
+
+constexpr int kXcds = 8;
+
+// The tile of workgroup `id`: an XCD's workgroups (id mod 8 equal) take a run
+// of consecutive tiles; tiles run down m within bands of `band` tiles of m,
+// then along n.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t nt, uint32_t mt, uint32_t& tn, uint32_t& tm)
+{
+    const uint32_t T = nt * mt, x = id % kXcds, q = T / kXcds, r = T % kXcds;
+    const uint32_t tile = x * q + min(x, r) + id / kXcds;
+    constexpr uint32_t band = 4;
+    const uint32_t g = tile / (band * nt), rest = tile - g * band * nt;
+    const uint32_t rows = min(band, mt - g * band);
+    tn = rest / rows;
+    tm = g * band + rest % rows;
+}
+
+template <int DT, int BN, int BM, int WN, int WM, int STAGES>
+__global__ __launch_bounds__(WN* WM * 64, 1) void project_tile_kernel(ProjectParams p)
+{
+    constexpr int NW = WN * WM;
+    constexpr int STAGE = (BN + BM) * 128;
+    constexpr int LN = BN / 8 / NW, LM = BM / 8 / NW;  // loads of a wave per step and side
+    constexpr int TN = BN / WN / 16, TM = BM / WM / 16;
+    static_assert(LN * 8 * NW == BN && LM * 8 * NW == BM && NW % 2 == 0, "loads divide evenly");
+    __shared__ __align__(1024) char lds[STAGES * STAGE];
+    const int lane = threadIdx.x & 63, v = uniform((int)(threadIdx.x >> 6));
+    const uint32_t nt = (uint32_t)((p.N + BN - 1) / BN), mt = (uint32_t)((p.M + BM - 1) / BM);
+    uint32_t tn, tm;
+    tile_of(blockIdx.x, nt, mt, tn, tm);
+    const int64_t n0 = (int64_t)tn * BN, m0 = (int64_t)tm * BM;
+    const int chunks = (int)(p.K * (DT == kF32 ? 4 : 2) / 16);
+    const int steps = (chunks + 7) / 8;
+    const int nrows = (int)min((int64_t)BN, p.N - n0), mrows = (int)min((int64_t)BM, p.M - m0);
+    const u32x4 rw = buffer_of(p.w + n0 * p.ws, (uint32_t)((nrows - 1) * p.ws) + (uint32_t)chunks * 16);
+    const u32x4 rh = buffer_of(p.h + m0 * p.hs, (uint32_t)((mrows - 1) * p.hs) + (uint32_t)chunks * 16);
+
+    // Load i of this wave: rows (i NW + v) 8 + lane / 8 of the side, at place
+    // lane % 8; rows past the end repeat the last (their results are not
+    // stored).  The row's parity pair (r / 2) % 8 does not depend on i.
+    const int place = lane & 7, x = place ^ (((v & 1) * 4 + (lane >> 4)) & 7);
+    uint32_t ow[LN], oh[LM];
+#pragma unroll
+    for (int i = 0; i < LN; ++i)
+        ow[i] = (uint32_t)min((i * NW + v) * 8 + (lane >> 3), nrows - 1) * (uint32_t)p.ws + (uint32_t)x * 16;
+#pragma unroll
+    for (int i = 0; i < LM; ++i)
+        oh[i] = (uint32_t)min((i * NW + v) * 8 + (lane >> 3), mrows - 1) * (uint32_t)p.hs + (uint32_t)x * 16;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_char*)lds;
+    auto issue = [&](int step) {
+        const uint32_t to = base + (uint32_t)(step % STAGES) * STAGE + (uint32_t)v * 1024;
+        const uint32_t soff = (uint32_t)step * 128;
+        const bool in = step * 8 + x < chunks;  // past K: zeros on both sides
+#pragma unroll
+        for (int i = 0; i < LN; ++i) load_to_lds(to + i * NW * 1024, rw, in ? ow[i] : 0x80000000u, soff);
+#pragma unroll
+        for (int i = 0; i < LM; ++i) load_to_lds(to + BN * 128 + i * NW * 1024, rh, in ? oh[i] : 0x80000000u, soff);
+    };
+    // Fragments: row l % 16 of a 16-row tile, chunk 4 g + l / 16.
+    const int wn = v % WN, wm = v / WN;
+    const int r16 = lane & 15, sw = r16 >> 1;
+    const int fw = (wn * TN * 16 + r16) * 128 + (((lane >> 4) ^ sw) * 16);
+    const int fh = BN * 128 + (wm * TM * 16 + r16) * 128 + (((lane >> 4) ^ sw) * 16);
+
+    f32x4 acc[TN][TM] = {};
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < steps) issue(s);
+    for (int s = 0; s < steps; ++s) {
+        if (STAGES > 2 && s + STAGES - 2 < steps)
+            wait_loads_and_meet<(STAGES - 2) * (LN + LM)>();
+        else
+            wait_loads_and_meet<0>();
+        if (s + STAGES - 1 < steps) issue(s + STAGES - 1);
+        const char* st = lds + (s % STAGES) * STAGE;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            u32x4 a[TN], b[TM];
+#pragma unroll
+            for (int i = 0; i < TN; ++i) a[i] = *(const u32x4*)(st + ((fw + i * 2048) ^ (g * 64)));
+#pragma unroll
+            for (int j = 0; j < TM; ++j) b[j] = *(const u32x4*)(st + ((fh + j * 2048) ^ (g * 64)));
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j) acc[i][j] = mfma_group<DT>(a[i], b[j], acc[i][j]);
+        }
+    }
+    // Results pass through LDS, JG of the TM tile rows of every wave at a
+    // time, so that whole rows of n are finished and stored together (and the
+    // epilogue's code is there once).
+    constexpr int PITCH = BN * 4 + 16;  // the 16 spread the 16 rows of a tile over the banks
+    constexpr int FIT = STAGES * STAGE / (WM * 16 * PITCH);
+    constexpr int JG = FIT >= TM ? TM : (FIT >= 4 && TM % 4 == 0 ? 4 : (FIT >= 2 && TM % 2 == 0 ? 2 : 1));
+    static_assert(FIT >= 1, "a tile row of every wave fits");
+#pragma unroll
+    for (int j0 = 0; j0 < TM; j0 += JG) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < JG; ++j)
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+                *(f32x4*)(lds + ((wm * JG + j) * 16 + r16) * PITCH + ((wn * TN + i) * 16 + 4 * (lane >> 4)) * 4) =
+                    acc[i][j0 + j];
+        __syncthreads();
+#pragma unroll 1
+        for (int e = threadIdx.x; e < WM * JG * 16 * (BN / 4); e += NW * 64) {
+            const int row = e / (BN / 4), n4 = e % (BN / 4);
+            const int m = ((row / (JG * 16)) * TM + j0) * 16 + row % (JG * 16);
+            project_store<DT>(p, m0 + m, n0 + 4 * n4, *(const f32x4*)(lds + row * PITCH + n4 * 16));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Too few tiles to fill the device: eight waves split k among them.  A
+// workgroup makes a 16 (n) x BM (m) tile; wave v takes the 128-byte pieces
+// v, v + 8, ... of k through an LDS ring of its own (STAGES pieces, no
+// barriers), and the partial tiles meet in LDS at the end.
+// ---------------------------------------------------------------------------
+constexpr int kSplitWaves = 8;
+
+// The wave's own loads but the last N have arrived, and its LDS reads have
+// returned.
+template <int N>
+__device__ __forceinline__ void wait_own_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+}
+
+template <int DT, int BM, int STAGES>
+__global__ __launch_bounds__(kSplitWaves * 64, 1) void project_split_kernel(ProjectParams p)
+{
+    constexpr int STAGE = (16 + BM) * 128;
+    constexpr int LM = BM / 8, L = 2 + LM, TM = BM / 16;
+    __shared__ __align__(1024) char lds[kSplitWaves * STAGES * STAGE];
+    static_assert(kSplitWaves * TM * 1024 <= (int)sizeof(lds), "partial tiles fit");
+    const int lane = threadIdx.x & 63, v = uniform((int)(threadIdx.x >> 6));
+    const uint32_t nt = (uint32_t)((p.N + 15) / 16);
+    const int64_t n0 = (int64_t)(blockIdx.x % nt) * 16, m0 = (int64_t)(blockIdx.x / nt) * BM;
+    const int chunks = (int)(p.K * (DT == kF32 ? 4 : 2) / 16);
+    const int pieces = (chunks + 7) / 8;
+    const int mine = pieces > v ? (pieces - v + kSplitWaves - 1) / kSplitWaves : 0;
+    const int nrows = (int)min((int64_t)16, p.N - n0), mrows = (int)min((int64_t)BM, p.M - m0);
+    const u32x4 rw = buffer_of(p.w + n0 * p.ws, (uint32_t)((nrows - 1) * p.ws) + (uint32_t)chunks * 16);
+    const u32x4 rh = buffer_of(p.h + m0 * p.hs, (uint32_t)((mrows - 1) * p.hs) + (uint32_t)chunks * 16);
+    // As in the tile kernel, with eight rows per load: r / 2 mod 8 is
+    // (4 i + lane / 16) mod 8 for load i.
+    uint32_t ow[2], oh[LM];
+    int x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = (lane & 7) ^ ((4 * i + (lane >> 4)) & 7);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        ow[i] = (uint32_t)min(i * 8 + (lane >> 3), nrows - 1) * (uint32_t)p.ws + (uint32_t)x[i] * 16;
+#pragma unroll
+    for (int i = 0; i < LM; ++i)
+        oh[i] = (uint32_t)min(i * 8 + (lane >> 3), mrows - 1) * (uint32_t)p.hs + (uint32_t)x[i & 1] * 16;
+    const uint32_t ring = (uint32_t)(uintptr_t)(lds_char*)lds + (uint32_t)(v * STAGES) * STAGE;
+    auto issue = [&](int s) {
+        const uint32_t to = ring + (uint32_t)(s % STAGES) * STAGE;
+        const int piece = v + s * kSplitWaves;
+        const uint32_t soff = (uint32_t)piece * 128;
+        const bool in[2] = {piece * 8 + x[0] < chunks, piece * 8 + x[1] < chunks};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load_to_lds(to + i * 1024, rw, in[i] ? ow[i] : 0x80000000u, soff);
+#pragma unroll
+        for (int i = 0; i < LM; ++i) load_to_lds(to + 2048 + i * 1024, rh, in[i & 1] ? oh[i] : 0x80000000u, soff);
+    };
+    const int r16 = lane & 15;
+    const int f = r16 * 128 + (((lane >> 4) ^ (r16 >> 1)) * 16);
+    f32x4 acc[TM] = {};
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < mine) issue(s);
+    for (int s = 0; s < mine; ++s) {
+        if (s + STAGES - 1 < mine) {
+            wait_own_loads<63>();  // the reads of the stage about to be overwritten
+            issue(s + STAGES - 1);
+            wait_own_loads<(STAGES - 1) * L>();
+        } else {
+            wait_own_loads<0>();
+        }
+        const char* st = lds + (v * STAGES + s % STAGES) * STAGE;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const u32x4 a = *(const u32x4*)(st + (f ^ (g * 64)));
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+                acc[j] = mfma_group<DT>(a, *(const u32x4*)(st + 2048 + j * 2048 + (f ^ (g * 64))), acc[j]);
+        }
+    }
+    __syncthreads();  // every wave has read its last stage
+    f32x4* part = (f32x4*)lds;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) part[(v * TM + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < TM * 64; e += kSplitWaves * 64) {
+        f32x4 z = part[e];
+#pragma unroll
+        for (int w = 1; w < kSplitWaves; ++w) z += part[w * TM * 64 + e];
+        const int l = e & 63;
+        project_store<DT>(p, m0 + 16 * (e >> 6) + (l & 15), n0 + 4 * (l >> 4), z);
+    }
+}
+
 }  // namespace nucleus
