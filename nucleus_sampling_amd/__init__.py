@@ -13,7 +13,6 @@ The C ABI, with the semantics of every argument, is ``include/nucleus.h``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -392,40 +391,51 @@ def spec_verify(target_probs: torch.Tensor, draft_probs: torch.Tensor, draft_tok
 
 _CODES = {torch.float32: NUCLEUS_F32, torch.bfloat16: NUCLEUS_BF16, torch.float16: NUCLEUS_F16}
 _ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "softcap": 4}
-_NO_SCOPE = contextlib.nullcontext()
+# The handle of a device's current stream, without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _scope(dev, stream):
-    """(stream, context): the stream a call launches on, and a context under
-    which the call's own allocations and conversions are made on that stream
-    and device (a no-op when they are the current ones)."""
+def _on(dev, stream, call, *args):
+    """``call(handle of the stream to launch on, *args)``, with the call's own
+    allocations and conversions made on that stream and device."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(_raw_stream(dev.index), *args)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-        if dev.index == torch.cuda.current_device():
-            return stream, _NO_SCOPE
     elif stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    return stream, torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream, *args)
 
 
-def _no_grad(name, *tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise NucleusError(f"{name} is for inference: it has no backward pass; call it under torch.no_grad() or detach its inputs")
+def _inference_only(name):
+    return NucleusError(f"{name} is for inference: it has no backward pass; call it under torch.no_grad() or "
+                        "detach its inputs")
 
 
-def _matrix(t, name, dev=None):
-    """Check that ``t`` is a 2-D GPU tensor (on ``dev``) with a dense last
-    dimension; rows that overlap or repeat are copied apart."""
-    if not torch.is_tensor(t) or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D tensor")
+def _on_gpu(t, name):
     if not t.is_cuda:
         raise NucleusError(f"{name} must be on the GPU: this library has no CPU path")
-    if dev is not None and t.device != dev:
+    return t.device
+
+
+def _matrix(t, name, dev):
+    """A 2-D tensor on ``dev`` with a dense last dimension, as (tensor, rows,
+    columns, elements between rows); rows that overlap or repeat are copied
+    apart."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    (rows, cols), (apart, step) = t.shape, t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.contiguous() if rows > 1 and t.stride(0) < cols else t
+    if rows <= 1:
+        apart = cols
+    elif apart < cols:
+        t, apart = t.contiguous(), cols
+    return t, rows, cols, apart
 
 
 def project(hidden: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -445,52 +455,57 @@ def project(hidden: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     ``residual`` itself.  Launches on ``stream`` (default: the current
     stream) and returns without synchronising.  Inference only: inputs that
     autograd would have to follow are refused."""
-    dev = hidden.device
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}, got {activation!r}")
     if hidden.dtype not in _CODES:
         raise TypeError(f"hidden must be float32, bfloat16 or float16, got {hidden.dtype}")
     if weight.dtype != hidden.dtype:
         raise TypeError(f"weight must have hidden's type {hidden.dtype}, got {weight.dtype}")
-    _no_grad("project", hidden, weight, bias, residual)
-    if not hidden.is_cuda:
-        raise NucleusError("hidden must be on the GPU: this library has no CPU path")
-    with _scope(dev, stream)[1]:
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        hidden, weight = _matrix(hidden, "hidden"), _matrix(weight, "weight", dev)
-        M, K = hidden.shape
-        N = weight.shape[0]
-        if weight.shape[1] != K or K < 1:
-            raise ValueError(f"hidden {tuple(hidden.shape)} and weight {tuple(weight.shape)} must share K >= 1")
-        opt = _ProjectOptions()
-        opt.dtype = _CODES[hidden.dtype]
-        opt.activation = _ACTIVATIONS[activation]
-        opt.softcap = softcap
-        opt.stream = s.cuda_stream
-        if bias is not None:
-            if bias.shape != (N,) or bias.device != dev or bias.dtype not in (hidden.dtype, torch.float32):
-                raise ValueError(f"bias must be a [{N}] tensor of {hidden.dtype} or float32 on {dev}")
-            bias = bias.contiguous()
-            opt.bias, opt.bias_dtype = bias.data_ptr(), _CODES[bias.dtype]
-        if out is None:
-            out = torch.empty((M, N), dtype=hidden.dtype if out_dtype is None else out_dtype, device=dev)
-        elif out.shape != (M, N) or out.device != dev or (out_dtype is not None and out.dtype != out_dtype) or (
-                N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
-            raise ValueError(f"out must be a [{M}, {N}] tensor on {dev}, of out_dtype and with rows apart and dense")
-        if out.dtype not in (hidden.dtype, torch.float32):
-            raise TypeError(f"the output must be {hidden.dtype} or float32, got {out.dtype}")
-        opt.out_dtype = _CODES[out.dtype]
-        if residual is not None:
-            if residual.dtype not in (hidden.dtype, torch.float32) or residual.shape != (M, N):
-                raise ValueError(f"residual must be a [{M}, {N}] tensor of {hidden.dtype} or float32")
-            residual = _matrix(residual, "residual", dev)
-            opt.residual, opt.residual_dtype = residual.data_ptr(), _CODES[residual.dtype]
-            opt.residual_stride = residual.stride(0) if M > 1 else N
-        opt.hidden_stride = hidden.stride(0) if M > 1 else K
-        opt.weight_stride = weight.stride(0) if N > 1 else K
-        opt.out_stride = out.stride(0) if M > 1 else N
-        rc = lib().nucleus_project(hidden.data_ptr(), weight.data_ptr(), M, N, K, out.data_ptr(), ctypes.byref(opt))
-    _check(rc, "nucleus_project")
+    if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad
+                                    or (bias is not None and bias.requires_grad)
+                                    or (residual is not None and residual.requires_grad)):
+        raise _inference_only("project")
+    dev = _on_gpu(hidden, "hidden")
+    return _on(dev, stream, _project, dev, hidden, weight, bias, residual, activation, softcap, out_dtype, out)
+
+
+def _project(handle, dev, hidden, weight, bias, residual, activation, softcap, out_dtype, out):
+    dtype = hidden.dtype
+    code = _CODES[dtype]
+    hidden, M, K, hs = _matrix(hidden, "hidden", dev)
+    weight, N, Kw, ws = _matrix(weight, "weight", dev)
+    if Kw != K or K < 1:
+        raise ValueError(f"hidden [{M}, {K}] and weight [{N}, {Kw}] must share K >= 1")
+    bp = rp = None
+    bcode = rcode = rs = 0
+    if bias is not None:
+        bcode = _CODES.get(bias.dtype, -1)
+        if bias.shape != (N,) or bias.device != dev or bcode not in (code, NUCLEUS_F32):
+            raise ValueError(f"bias must be a [{N}] tensor of {dtype} or float32 on {dev}")
+        bias = bias.contiguous()
+        bp = bias.data_ptr()
+    if residual is not None:
+        rcode = _CODES.get(residual.dtype, -1)
+        residual, Mr, Nr, rs = _matrix(residual, "residual", dev)
+        if (Mr, Nr) != (M, N) or rcode not in (code, NUCLEUS_F32):
+            raise ValueError(f"residual must be a [{M}, {N}] tensor of {dtype} or float32")
+        rp = residual.data_ptr()
+    if out is None:
+        ocode = code if out_dtype is None else _CODES.get(out_dtype, -1)
+        if ocode not in (code, NUCLEUS_F32):
+            raise TypeError(f"the output must be {dtype} or float32, got {out_dtype}")
+        out = torch.empty((M, N), dtype=out_dtype or dtype, device=dev)
+        os_ = N
+    else:
+        ocode = _CODES.get(out.dtype, -1)
+        if out.shape != (M, N) or out.device != dev or (out_dtype is not None and out.dtype != out_dtype) or (
+                N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N) or ocode not in (code, NUCLEUS_F32):
+            raise ValueError(f"out must be a [{M}, {N}] tensor of {out_dtype or dtype} or float32 on {dev} with dense "
+                             "rows apart from each other")
+        os_ = out.stride(0) if M > 1 else N
+    opt = _ProjectOptions(code, ocode, _ACTIVATIONS[activation], softcap, handle, bp, rp, bcode, rcode, hs, ws, os_, rs)
+    _check((_lib or lib()).nucleus_project(hidden.data_ptr(), weight.data_ptr(), M, N, K, out.data_ptr(),
+                                           ctypes.byref(opt)), "nucleus_project")
     return out
 
 
@@ -501,20 +516,30 @@ class GivenResult(NamedTuple):
     probs: Optional[torch.Tensor]    # float32 [B, V] or None
 
 
-def _uniforms(u, shapes, dev):
+def _per_row(t, B, dtype, name, dev):
+    """``_vec`` with a short way for what needs no conversion."""
+    if torch.is_tensor(t) and t.dtype is dtype and t.device == dev and t.numel() == B and t.is_contiguous():
+        return t.data_ptr(), t
+    t = _vec(t, B, dtype, name, dev)
+    return (None if t is None else t.data_ptr()), t
+
+
+def _uniforms(u, dev):
     if not torch.is_tensor(u):
         u = torch.as_tensor(u, dtype=torch.float64)
-    if u.dtype not in (torch.float32, torch.float64):
+    if u.dtype is torch.float32:
+        code = NUCLEUS_F32
+    elif u.dtype is torch.float64:
+        code = NUCLEUS_F64
+    else:
         raise TypeError(f"uniforms must be float32 or float64, got {u.dtype}")
-    if tuple(u.shape) not in shapes and (u.dim() != 2 or (u.shape[0], None) not in shapes or u.shape[1] < 1):
-        raise ValueError(f"uniforms of shape {tuple(u.shape)} do not fit the batch")
-    return u.to(dev).contiguous(), NUCLEUS_F32 if u.dtype == torch.float32 else NUCLEUS_F64
+    return (u if u.device == dev else u.to(dev)).contiguous(), code
 
 
 def _output(t, shape, dtype, name, dev):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
         raise ValueError(f"out.{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
     return t
 
@@ -535,35 +560,34 @@ def sample_given(logits: torch.Tensor, temperature, top_p, uniforms, top_k=None,
     stream) and returns without synchronising."""
     if not torch.is_tensor(logits) or logits.dtype not in _CODES:
         raise TypeError("logits must be a float32, bfloat16 or float16 tensor")
-    _no_grad("sample_given", logits)
-    if not logits.is_cuda:
-        raise NucleusError("logits must be on the GPU: this library has no CPU path")
-    dev = logits.device
-    with _scope(dev, stream)[1]:
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        logits = _matrix(logits, "logits")
-        B, V = logits.shape
-        U, ucode = _uniforms(uniforms, ((B,), (B, None)), dev)
-        T = _vec(temperature, B, torch.float32, "temperature", dev)
-        P = _vec(top_p, B, torch.float32, "top_p", dev)
-        K = _vec(top_k, B, torch.int32, "top_k", dev)
-        MP = _vec(min_p, B, torch.float32, "min_p", dev)
-        o = out if out is not None else GivenResult(None, None, None, None)
-        res = GivenResult(_output(o.token, U.shape, torch.int32, "token", dev),
-                          _output(o.keep_count, (B,), torch.int32, "keep_count", dev),
-                          _output(o.logprob, U.shape, torch.float32, "logprob", dev),
-                          _output(o.probs, (B, V), torch.float32, "probs", dev)
-                          if want_probs or o.probs is not None else None)
-        opt = _Options()
-        opt.dtype = _CODES[logits.dtype]
-        opt.stream = s.cuda_stream
-        opt.row_stride = logits.stride(0) if B > 1 else V
-        rc = lib().nucleus_sample_given(
-            logits.data_ptr(), B, V, T.data_ptr(), P.data_ptr(), None if K is None else K.data_ptr(),
-            None if MP is None else MP.data_ptr(), U.data_ptr(), ucode, U.shape[1] if U.dim() == 2 else 1,
-            res.token.data_ptr(), res.keep_count.data_ptr(), res.logprob.data_ptr(),
-            None if res.probs is None else res.probs.data_ptr(), ctypes.byref(opt))
-    _check(rc, "nucleus_sample_given")
+    if logits.requires_grad and torch.is_grad_enabled():
+        raise _inference_only("sample_given")
+    dev = _on_gpu(logits, "logits")
+    return _on(dev, stream, _sample_given, dev, logits, temperature, top_p, uniforms, top_k, min_p, want_probs, out)
+
+
+def _sample_given(handle, dev, logits, temperature, top_p, uniforms, top_k, min_p, want_probs, out):
+    logits, B, V, stride = _matrix(logits, "logits", dev)
+    U, ucode = _uniforms(uniforms, dev)
+    shape = U.shape
+    N = 1 if len(shape) == 1 else shape[-1]
+    if len(shape) not in (1, 2) or shape[0] != B or N < 1:
+        raise ValueError(f"uniforms must be [{B}] or [{B}, N], got {tuple(shape)}")
+    tp, T = _per_row(temperature, B, torch.float32, "temperature", dev)
+    pp, P = _per_row(top_p, B, torch.float32, "top_p", dev)
+    kp, K = (None, None) if top_k is None else _per_row(top_k, B, torch.int32, "top_k", dev)
+    mp, MP = (None, None) if min_p is None else _per_row(min_p, B, torch.float32, "min_p", dev)
+    o = out if out is not None else GivenResult(None, None, None, None)
+    res = GivenResult(_output(o.token, shape, torch.int32, "token", dev),
+                      _output(o.keep_count, (B,), torch.int32, "keep_count", dev),
+                      _output(o.logprob, shape, torch.float32, "logprob", dev),
+                      _output(o.probs, (B, V), torch.float32, "probs", dev)
+                      if want_probs or o.probs is not None else None)
+    opt = _Options(_CODES[logits.dtype], 0, handle, stride)
+    _check((_lib or lib()).nucleus_sample_given(
+        logits.data_ptr(), B, V, tp, pp, kp, mp, U.data_ptr(), ucode, N, res.token.data_ptr(),
+        res.keep_count.data_ptr(), res.logprob.data_ptr(), None if res.probs is None else res.probs.data_ptr(),
+        ctypes.byref(opt)), "nucleus_sample_given")
     return res
 
 
@@ -578,26 +602,31 @@ def spec_verify_given(target_probs: torch.Tensor, draft_probs: torch.Tensor, dra
             raise ValueError(f"{name} must be a float32 [B, V] tensor on the GPU")
     if target_probs.shape != draft_probs.shape or target_probs.device != draft_probs.device:
         raise ValueError("target_probs and draft_probs must have the same shape and device")
-    _no_grad("spec_verify_given", target_probs, draft_probs)
-    B, V = target_probs.shape
+    if torch.is_grad_enabled() and (target_probs.requires_grad or draft_probs.requires_grad):
+        raise _inference_only("spec_verify_given")
     dev = target_probs.device
-    with _scope(dev, stream)[1]:
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        Pt, Qt = target_probs.contiguous(), draft_probs.contiguous()
-        D = _vec(draft_token, B, torch.int32, "draft_token", dev)
-        U, ucode = _uniforms(uniforms, ((B, 2),), dev)
-        o = out if out is not None else SpecResult(None, None)
-        res = SpecResult(_output(o.token, (B,), torch.int32, "token", dev),
-                         _output(o.accepted, (B,), torch.int32, "accepted", dev))
-        # A workspace of the call's own: stream-ordered when it is freed, and
-        # under graph capture the graph's.
-        ws = torch.empty(lib().nucleus_spec_given_workspace_bytes(B, V), dtype=torch.uint8, device=dev)
-        opt = _Options()
-        opt.stream = s.cuda_stream
-        opt.workspace, opt.workspace_bytes = ws.data_ptr(), ws.numel()
-        rc = lib().nucleus_spec_verify_given(Pt.data_ptr(), Qt.data_ptr(), D.data_ptr(), B, V, U.data_ptr(), ucode,
-                                             res.token.data_ptr(), res.accepted.data_ptr(), ctypes.byref(opt))
-    _check(rc, "nucleus_spec_verify_given")
+    return _on(dev, stream, _spec_verify_given, dev, target_probs, draft_probs, draft_token, uniforms, out)
+
+
+def _spec_verify_given(handle, dev, target_probs, draft_probs, draft_token, uniforms, out):
+    B, V = target_probs.shape
+    Pt, Qt = target_probs.contiguous(), draft_probs.contiguous()
+    dp, D = _per_row(draft_token, B, torch.int32, "draft_token", dev)
+    U, ucode = _uniforms(uniforms, dev)
+    if U.shape != (B, 2):
+        raise ValueError(f"uniforms must be [{B}, 2], got {tuple(U.shape)}")
+    o = out if out is not None else SpecResult(None, None)
+    res = SpecResult(_output(o.token, (B,), torch.int32, "token", dev),
+                     _output(o.accepted, (B,), torch.int32, "accepted", dev))
+    # A workspace of the call's own: its memory is reused in stream order, and
+    # under graph capture it is the graph's.
+    L = _lib or lib()
+    need = L.nucleus_spec_given_workspace_bytes(B, V)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    opt = _Options(0, 0, handle, 0, ws.data_ptr(), need)
+    _check(L.nucleus_spec_verify_given(Pt.data_ptr(), Qt.data_ptr(), dp, B, V, U.data_ptr(), ucode,
+                                       res.token.data_ptr(), res.accepted.data_ptr(), ctypes.byref(opt)),
+           "nucleus_spec_verify_given")
     return res
 
 

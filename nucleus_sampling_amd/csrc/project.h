@@ -64,6 +64,21 @@ __device__ __forceinline__ f32x4 mfma_group(u32x4 w, u32x4 h, f32x4 acc)
     }
 }
 
+// fp32 products are summed in two levels, 32 of k by the matrix instructions
+// from 0 and those sums in turn: a quarter-K chain of additions would leave
+// about three times the rounding error.  16-bit products, whose instructions
+// take 32 of k at once, go on from the running sum.
+template <int DT>
+__device__ __forceinline__ f32x4 start_of(f32x4 acc)
+{
+    return DT == kF32 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc;
+}
+template <int DT>
+__device__ __forceinline__ f32x4 joined(f32x4 acc, f32x4 sum)
+{
+    return DT == kF32 ? acc + sum : sum;
+}
+
 __device__ __forceinline__ float activate(int act, float cap, float z)
 {
     switch (act) {
@@ -186,6 +201,7 @@ __global__ __launch_bounds__(kAnyThreads) void project_any_kernel(ProjectParams 
         }
         __syncthreads();
         if (k0 + KT < p.K) fetch(k0 + KT);
+        f32x4 sum[4];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             const int off = (g * 4 + (lane >> 4)) * 16;
@@ -193,9 +209,11 @@ __global__ __launch_bounds__(kAnyThreads) void project_any_kernel(ProjectParams 
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const u32x4 b = *(const u32x4*)(lds + (kAnyTile + 16 * u + (lane & 15)) * ROWB + off);
-                acc[u] = mfma_group<DT>(a, b, acc[u]);
+                sum[u] = mfma_group<DT>(a, b, g == 0 ? start_of<DT>(acc[u]) : sum[u]);
             }
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[u] = joined<DT>(acc[u], sum[u]);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -319,6 +337,11 @@ __global__ __launch_bounds__(WN* WM * 64, 1) void project_tile_kernel(ProjectPar
             wait_loads_and_meet<0>();
         if (s + STAGES - 1 < steps) issue(s + STAGES - 1);
         const char* st = lds + (s % STAGES) * STAGE;
+        f32x4 sum[TN][TM];
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) sum[i][j] = start_of<DT>(acc[i][j]);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             u32x4 a[TN], b[TM];
@@ -329,8 +352,12 @@ __global__ __launch_bounds__(WN* WM * 64, 1) void project_tile_kernel(ProjectPar
 #pragma unroll
             for (int i = 0; i < TN; ++i)
 #pragma unroll
-                for (int j = 0; j < TM; ++j) acc[i][j] = mfma_group<DT>(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < TM; ++j) sum[i][j] = mfma_group<DT>(a[i], b[j], sum[i][j]);
         }
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) acc[i][j] = joined<DT>(acc[i][j], sum[i][j]);
     }
     // Results pass through LDS, JG of the TM tile rows of every wave at a
     // time, so that whole rows of n are finished and stored together (and the
@@ -428,13 +455,18 @@ __global__ __launch_bounds__(kSplitWaves * 64, 1) void project_split_kernel(Proj
             wait_own_loads<0>();
         }
         const char* st = lds + (v * STAGES + s % STAGES) * STAGE;
+        f32x4 sum[TM];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) sum[j] = start_of<DT>(acc[j]);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             const u32x4 a = *(const u32x4*)(st + (f ^ (g * 64)));
 #pragma unroll
             for (int j = 0; j < TM; ++j)
-                acc[j] = mfma_group<DT>(a, *(const u32x4*)(st + 2048 + j * 2048 + (f ^ (g * 64))), acc[j]);
+                sum[j] = mfma_group<DT>(a, *(const u32x4*)(st + 2048 + j * 2048 + (f ^ (g * 64))), sum[j]);
         }
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[j] = joined<DT>(acc[j], sum[j]);
     }
     __syncthreads();  // every wave has read its last stage
     f32x4* part = (f32x4*)lds;
