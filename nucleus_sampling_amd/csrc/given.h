@@ -10,19 +10,19 @@
 // are carried to about 1e-13 (doubles and 45-bit integers), not to the 1e-7
 // that the race needs.
 //
-// Weights.  y = x s with s = 16 log2(e) / T: a cell a = floor(y) spans a
-// sixteenth of an octave of weight, and a token of cell a weighs
+// Weights.  y = x s with s = 32 log2(e) / T: a cell a = rint(y) spans a
+// thirty-second of an octave of weight, and a token of cell a weighs
 //
-//     2^((a + 1/2)/16) * 2^(h/16),   h = y - a - 1/2 in [-1/2, 1/2),
+//     2^(a/32) * 2^(h/32),   h = y - a in [-1/2, 1/2],
 //
-// the second factor by its Taylor polynomial of degree 5 (|h ln2 / 16| <
-// 0.0217, so the first term left out is below 1.5e-13).  Cells do not move
-// with the row max, so one pass finds the max and histograms the row.  A
-// histogram slot sums the second factors as integers of `bits` fractional
-// bits (62 - ceil(log2 V), at most 50): exact in any order.  The window holds
-// 1024 cells (64 octaves) below the max of the first tokens loaded and 1024
-// above it; what is further down weighs less than 2^-64 of the max each and
-// is counted only.  A row whose max lies above the window takes the pass again.
+// the second factor by a polynomial of degree 4 (off by less than 8e-14).
+// Cells do not move with the row max, so one pass finds the max and
+// histograms the row.  A histogram slot sums the second factors as integers of
+// `bits` fractional bits (62 - ceil(log2 V), at most 50): exact in any order.
+// The window holds 2048 cells (64 octaves) below the max of the first tokens
+// loaded and 2048 above it; what is further down weighs less than 2^-64 of the
+// max each and is counted only.  A row whose max lies above the window takes
+// the pass again.
 //
 // The cuts.  With the cells ranked down from the max's (rank 0), top-k or
 // min-p cut through one bottom cell rb.  The survivors' mass S lies between
@@ -46,12 +46,15 @@ namespace nucleus {
 
 constexpr int kGivenThreads = 1024;
 constexpr int kGivenWaves = kGivenThreads / kWave;
-constexpr int kSlots = 2048;      // histogram window
-constexpr int kSlotsBelow = 1024; // of it, below the anchor
+constexpr int kOctave = 32;       // cells per octave of weight
+constexpr int kSlots = 4096;      // histogram window
+constexpr int kSlotsBelow = 2048; // of it, below the anchor: 64 octaves
 constexpr int kGivenCap = 8192;   // listed tokens of undecided cells
 constexpr int kSubs = 1024;       // index segments, at most
+constexpr int kSubSteps = 8;      // steps of a segment, at least
 constexpr int kRankNone = 0x7FFFFFFF;
-constexpr int kRankZero = 1 << 15;  // a rank whose weight is 0 in double (2^-2048)
+constexpr int kRankZero = 1 << 16;  // a rank whose weight is 0 in double (2^-2048)
+constexpr double kLn2 = 0.69314718055994530942;
 
 struct GivenParams {
     const void* logits;        // [B, stride]
@@ -67,15 +70,18 @@ struct GivenParams {
     int32_t* out_count;        // [B]
     float* out_logprob;        // [B, N] or null
     float* out_probs;          // [B, V] or null
-    int vec;                   // rows start on 16-byte boundaries
     int bits;                  // fractional bits of in-cell weights
 };
 
-// 2^(i/16), i = 0 .. 15, correctly rounded.
-__device__ constexpr double kRoot16[16] = {
-    1.0, 1.0442737824274138, 1.0905077326652577, 1.1387886347566916, 1.189207115002721, 1.241857812073484,
-    1.2968395546510096, 1.3542555469368927, 1.4142135623730951, 1.4768261459394993, 1.5422108254079407,
-    1.6104903319492543, 1.681792830507429, 1.7562521603732995, 1.8340080864093424, 1.9152065613971474};
+// 2^(i/32), i = 0 .. 31, correctly rounded.
+__device__ constexpr double kRoot[kOctave] = {
+    1.0, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237, 1.0905077326652577, 1.1143867425958924,
+    1.1387886347566916, 1.1637248587775775, 1.189207115002721, 1.215247359980469, 1.241857812073484,
+    1.2690509571917332, 1.2968395546510096, 1.3252366431597413, 1.3542555469368927, 1.383909881963832,
+    1.4142135623730951, 1.4451808069770467, 1.4768261459394993, 1.5091644275934228, 1.5422108254079407,
+    1.5759808451078865, 1.6104903319492543, 1.645755478153965, 1.681792830507429, 1.718619298122478,
+    1.7562521603732995, 1.7947090750031072, 1.8340080864093424, 1.8741676341103, 1.9152065613971474,
+    1.9571441241754002};
 
 // The row's lattice.
 struct Cells {
@@ -91,37 +97,55 @@ __device__ __forceinline__ int slot_of(const Cells& c, float x, double& h)
 {
 #pragma clang fp contract(off)
     const double y = (double)x * c.s;
-    const double a = floor(y);
-    h = (y - a) - 0.5;
+    const double a = rint(y);
+    h = y - a;
     return cvt_i32_sat(a - c.base);
 }
 
-// 2^(h/16) by Taylor's polynomial, |h| <= 1/2.
+// 2^(h/32) for |h| <= 1/2: Taylor's polynomial of degree 5 with its last term
+// replaced by the cubic nearest to it there (h^5 ~ (20 r^2 h^3 - 5 r^4 h)/16,
+// r = 1/2, by the fifth Chebyshev polynomial): degree 4, off by less than
+// 8e-14.
+constexpr double kL = kLn2 / kOctave, kL5 = kL * kL * kL * kL * kL / 120;
+constexpr double kP1 = kL - kL5 * 5 / 256, kP2 = kL * kL / 2, kP3 = kL * kL * kL / 6 + kL5 * 20 / 64,
+                 kP4 = kL * kL * kL * kL / 24;
+
 __device__ __forceinline__ double in_cell(double h)
 {
-    constexpr double l = 0.69314718055994530942 / 16.0;
-    constexpr double c1 = l, c2 = l * l / 2, c3 = l * l * l / 6, c4 = l * l * l * l / 24, c5 = l * l * l * l * l / 120;
-    return fma(fma(fma(fma(fma(c5, h, c4), h, c3), h, c2), h, c1), h, 1.0);
+    return fma(fma(fma(fma(kP4, h, kP3), h, kP2), h, kP1), h, 1.0);
 }
 
-// The integer q 2^bits, rounded to nearest, for q 2^bits < 2^52: adding 2^52
-// leaves it in the low bits of the double.
-__device__ __forceinline__ uint64_t fixed_point(double q, double scale)
+// The same times 2^bits, rounded to an integer (below 2^52: added to 2^52, it
+// is in the low bits of the double).
+struct Fixed {
+    double c1, c2, c3, c4, c0;
+    __device__ explicit Fixed(double scale)
+        : c1(uniform(kP1 * scale)), c2(uniform(kP2 * scale)), c3(uniform(kP3 * scale)), c4(uniform(kP4 * scale)),
+          c0(uniform(scale + 0x1p52))
+    {
+    }
+    __device__ __forceinline__ uint64_t operator()(double h) const
+    {
+        return (uint64_t)__double_as_longlong(fma(fma(fma(fma(c4, h, c3), h, c2), h, c1), h, c0)) -
+               0x4330000000000000ull;
+    }
+};
+
+// The integer nearest to v < 2^52.
+__device__ __forceinline__ uint64_t fixed_point(double v)
 {
-    return (uint64_t)__double_as_longlong(fma(q, scale, 0x1p52)) - 0x4330000000000000ull;
+    return (uint64_t)__double_as_longlong(v + 0x1p52) - 0x4330000000000000ull;
 }
 
-// 2^(-rank/16) for 0 <= rank; root: kRoot16 in LDS.
+// 2^(-rank/32) for 0 <= rank; root: kRoot in LDS.
 __device__ __forceinline__ double rank_weight(const double* root, int rank)
 {
-    const int r = min(rank, kRankZero);
-    return ldexp(root[(-r) & 15], (-r) >> 4);
+    const int r = -min(rank, kRankZero);
+    return ldexp(root[r & (kOctave - 1)], r >> 5);
 }
 
-template <int DT> struct Group;
-template <> struct Group<kF32> { static constexpr int N = 4; };
-template <> struct Group<kBF16> { static constexpr int N = 8; };
-template <> struct Group<kF16> { static constexpr int N = 8; };
+// A group: the 16 bytes of a row that a lane loads at a time.
+template <int DT> struct Group { static constexpr int N = DT == kF32 ? 4 : 8; };
 
 template <int DT>
 __device__ __forceinline__ float logit_at(const void* row, int64_t i)
@@ -151,18 +175,42 @@ __device__ __forceinline__ void unpack(u32x4 v, float (&x)[Group<DT>::N])
     }
 }
 
-// Group g of the row (tokens N g .. N g + N - 1) widened to fp32; -inf past
-// the row's end.
+// The 16 bytes of group g.  VEC: rows start on 16-byte boundaries and hold
+// whole groups; a group past the end reads the last one.  Otherwise element
+// by element, the last element past the end.  The caller masks both.
+template <int DT, bool VEC>
+__device__ __forceinline__ u32x4 load_raw(const void* row, uint32_t g, uint32_t groups, int64_t V)
+{
+    if constexpr (VEC) {
+        return *((const u32x4*)row + min(g, groups - 1));
+    } else {
+        constexpr int N = Group<DT>::N;
+        u32x4 v;
+        if constexpr (DT == kF32) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = ((const uint32_t*)row)[min((int64_t)g * N + j, V - 1)];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t lo = ((const uint16_t*)row)[min((int64_t)g * N + 2 * j, V - 1)];
+                const uint32_t hi = ((const uint16_t*)row)[min((int64_t)g * N + 2 * j + 1, V - 1)];
+                v[j] = lo | hi << 16;
+            }
+        }
+        return v;
+    }
+}
+
+// Group g's tokens widened to fp32; -inf past the row's end (checked only
+// where `edge` says that the row may end here).
 template <int DT>
-__device__ __forceinline__ void load_group(const GivenParams& p, const void* row, uint32_t g, float (&x)[Group<DT>::N])
+__device__ __forceinline__ void tokens_of(u32x4 raw, uint32_t g, bool edge, int64_t V, float (&x)[Group<DT>::N])
 {
     constexpr int N = Group<DT>::N;
-    const int64_t i0 = (int64_t)g * N;
-    if (p.vec && i0 + N <= p.V) {
-        unpack<DT>(*((const u32x4*)row + g), x);
-    } else {
+    unpack<DT>(raw, x);
+    if (edge) {  // uniform
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = i0 + j < p.V ? logit_at<DT>(row, i0 + j) : -INFINITY;
+        for (int j = 0; j < N; ++j) x[j] = (int64_t)g * N + j < V ? x[j] : -INFINITY;
     }
 }
 
@@ -181,9 +229,44 @@ __device__ __forceinline__ Deal deal_out(int64_t V)
     Deal d;
     d.groups = (uint32_t)((V + Group<DT>::N - 1) / Group<DT>::N);
     d.steps = (d.groups + kGivenThreads - 1) / kGivenThreads;
-    d.sps = max(8u, (d.steps + kSubs / kGivenWaves - 1) / (kSubs / kGivenWaves));
+    d.sps = max((uint32_t)kSubSteps, (d.steps + kSubs / kGivenWaves - 1) / (kSubs / kGivenWaves));
     d.spw = (d.steps + d.sps - 1) / d.sps;
     return d;
+}
+
+// fn(step, group, tokens) over the wave's steps, in order, with the loads of
+// the next kAhead steps in flight (of two where they are made element by
+// element).  Every lane takes every step (past the row's end with tokens of
+// -inf).
+template <int DT, bool VEC, class Fn>
+__device__ __forceinline__ void stream_row(const void* row, const Deal& d, int64_t V, Fn fn)
+{
+    constexpr int kAhead = VEC ? 4 : 2;
+    const uint32_t lane = threadIdx.x & (kWave - 1), g0 = (threadIdx.x / kWave) * d.steps * kWave + lane;
+    u32x4 a[kAhead], b[kAhead];
+    auto fetch = [&](u32x4 (&to)[kAhead], uint32_t i) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            to[k] = load_raw<DT, VEC>(row, g0 + min(i + k, d.steps - 1) * kWave, d.groups, V);
+    };
+    auto take = [&](const u32x4 (&from)[kAhead], uint32_t i) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (i + k >= d.steps) return;  // uniform
+            const uint32_t g = g0 + (i + k) * kWave;
+            float x[Group<DT>::N];
+            tokens_of<DT>(from[k], g, uniform((int)((int64_t)(g - lane + kWave) * Group<DT>::N > V)) != 0, V, x);
+            fn(i + k, g, x);
+        }
+    };
+    fetch(a, 0);
+    for (uint32_t i = 0; i < d.steps; i += 2 * kAhead) {
+        fetch(b, i + kAhead);
+        take(a, i);
+        if (i + kAhead >= d.steps) break;
+        fetch(a, i + 2 * kAhead);
+        take(b, i + kAhead);
+    }
 }
 
 struct GivenShared {
@@ -193,7 +276,7 @@ struct GivenShared {
     double sub[kSubs];         // mass of each segment's surely kept tokens; then of the segments up to it (-1: empty)
     uint64_t subc[kSubs];      // mass of its kept listed tokens, at 2^-bits
     double pre[kSubs];         // mass of the segments before it
-    double root[16];
+    double root[kOctave];
     SelectShared sel;
     uint64_t red64[kGivenWaves];
     double redf[kGivenWaves];
@@ -201,7 +284,7 @@ struct GivenShared {
     // decided by one thread, read by all
     double s_above, a_lo, w_bottom;
     uint32_t n_above, n_window;
-    int r_lo, r_hi, cross;
+    int cross;
     uint64_t tc;
 };
 
@@ -237,7 +320,48 @@ enum : int {
     kGivenCells = 3,   // kept: by cells and the listed tokens
 };
 
-template <int DT>
+// What the first pass finds.
+struct FirstPass {
+    float m;         // max
+    bool bad;        // NaN or +inf seen (this thread)
+    bool over;       // a token above the window (this thread)
+    uint32_t tail;   // finite tokens below the window (this thread)
+    uint64_t best;   // greedy: (key, ~index) of this thread's max
+};
+
+enum : int { kPassMax = 0, kPassGreedy = 1, kPassHist = 2, kPassCount = 3 };
+
+template <int DT, bool VEC, int PASS>
+__device__ __forceinline__ FirstPass first_pass(const void* row, const Deal& d, int64_t V, const Cells& c,
+                                                const Fixed& fx, GivenShared& sh)
+{
+    FirstPass r = {-INFINITY, false, false, 0, 0};
+    stream_row<DT, VEC>(row, d, V, [&](uint32_t, uint32_t g, const float (&x)[Group<DT>::N]) {
+#pragma unroll
+        for (int j = 0; j < Group<DT>::N; ++j) {
+            r.bad |= !(x[j] < INFINITY);
+            r.m = fmaxf(r.m, x[j]);
+            if constexpr (PASS == kPassGreedy) {
+                const uint64_t pk = ((uint64_t)order_key(x[j]) << 32) | (uint32_t)~(uint32_t)(g * Group<DT>::N + j);
+                r.best = pk > r.best ? pk : r.best;
+            }
+            if constexpr (PASS >= kPassHist) {
+                double h;
+                const int sl = slot_of(c, x[j], h);
+                if ((uint32_t)sl < (uint32_t)kSlots && x[j] > -INFINITY) {
+                    atomicAdd((unsigned long long*)&sh.hist[sl], (unsigned long long)fx(h));
+                    if constexpr (PASS == kPassCount) atomicAdd(&sh.cnt[sl], 1u);
+                } else {
+                    r.over |= sl >= kSlots;
+                    if constexpr (PASS == kPassCount) r.tail += x[j] > -INFINITY;
+                }
+            }
+        }
+    });
+    return r;
+}
+
+template <int DT, bool VEC>
 __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
 {
     constexpr int GN = Group<DT>::N;
@@ -247,8 +371,8 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
     const size_t esz = DT == kF32 ? 4 : 2;
     const void* row = (const char*)p.logits + (size_t)b * (size_t)p.stride * esz;
     const Deal d = deal_out<DT>(p.V);
-    const uint32_t g_wave = (uint32_t)w * d.steps * kWave;
     const double scale = ldexp(1.0, p.bits), inv_scale = ldexp(1.0, -p.bits);
+    const Fixed fx(scale);
 
     const float T = p.temperature[b], P = p.top_p[b];
     const int K = p.top_k ? p.top_k[b] : 0;
@@ -258,7 +382,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
     // A histogram is needed where a cut has to be searched for.
     const bool want_hist = !greedy && P > 0.0f && (P < 1.0f || use_k);
 
-    if (t < 16) sh.root[t] = kRoot16[t];
+    if (t < kOctave) sh.root[t] = kRoot[t];
     for (int i = t; i < kSubs; i += kGivenThreads) {
         sh.sub[i] = 0.0;
         sh.subc[i] = 0;
@@ -267,30 +391,24 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
 
     // ---- pass 1: max, NaN / +inf, histogram -----------------------------
     Cells c;
-    c.s = (greedy || T == INFINITY) ? 0.0 : (16.0 * 1.4426950408889634074) / (double)T;
+    c.s = (greedy || T == INFINITY) ? 0.0 : (kOctave * 1.4426950408889634074) / (double)T;
     c.base = 0.0;
-    float m = -INFINITY;
-    uint64_t best = 0;      // greedy: (key, ~index) of the max
-    bool bad = false;
-    uint32_t tail = 0;      // finite tokens below the window, this thread
+    FirstPass f;
     float anchor = -INFINITY;
-    {
+    if (want_hist) {
         // The anchor: the max of every thread's first group.
         float x[GN];
-        const uint32_t g = g_wave + lane;
-        if (g < d.groups && want_hist) {
-            load_group<DT>(p, row, g, x);
+        const uint32_t g = (uint32_t)w * d.steps * kWave + lane;
+        tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
 #pragma unroll
-            for (int j = 0; j < GN; ++j) anchor = fmaxf(anchor, x[j]);
-        }
-        __syncthreads();
-        if (want_hist) anchor = block_reduce<kGivenThreads>(anchor, MaxF32(), (float*)sh.redf);
+        for (int j = 0; j < GN; ++j) anchor = fmaxf(anchor, x[j]);
+        anchor = block_reduce<kGivenThreads>(anchor, MaxF32(), (float*)sh.redf);
     }
     // At most two attempts: the second is anchored at the row's own max.
     for (int attempt = 0; attempt < 2; ++attempt) {
         const bool hist = want_hist && anchor > -INFINITY && anchor < INFINITY;
         if (hist) {
-            c.base = floor((double)anchor * c.s) - kSlotsBelow;
+            c.base = rint((double)anchor * c.s) - kSlotsBelow;
             for (int i = t; i < kSlots; i += kGivenThreads) {
                 sh.hist[i] = 0;
                 sh.cnt[i] = 0;
@@ -298,47 +416,26 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
             __syncthreads();
         }
         c = uniform(c);
-        tail = 0;
-        bool over = false;
-        for (uint32_t i = 0; i < d.steps; ++i) {
-            const uint32_t g = g_wave + i * kWave + lane;
-            if (g >= d.groups) break;
-            float x[GN];
-            load_group<DT>(p, row, g, x);
-#pragma unroll
-            for (int j = 0; j < GN; ++j) {
-                bad |= !(x[j] < INFINITY);  // NaN or +inf
-                m = fmaxf(m, x[j]);
-                if (greedy) {
-                    const uint64_t pk = ((uint64_t)order_key(x[j]) << 32) | (uint32_t)~(uint32_t)(g * GN + j);
-                    best = pk > best ? pk : best;
-                }
-                if (hist && x[j] > -INFINITY) {
-                    double h;
-                    const int sl = slot_of(c, x[j], h);
-                    if ((uint32_t)sl < (uint32_t)kSlots) {
-                        atomicAdd((unsigned long long*)&sh.hist[sl], (unsigned long long)fixed_point(in_cell(h), scale));
-                        if (use_k) atomicAdd(&sh.cnt[sl], 1u);
-                    } else if (sl < 0) {
-                        ++tail;
-                    } else {
-                        over = true;
-                    }
-                }
-            }
-        }
-        m = block_reduce<kGivenThreads>(m, MaxF32(), (float*)sh.redf);
-        const int again = block_reduce<kGivenThreads>((int)over, OrI32(), (int*)sh.redf);
-        if (!want_hist || (hist && !again) || !(m > -INFINITY && m < INFINITY)) break;
-        anchor = m;
+        if (hist && use_k)
+            f = first_pass<DT, VEC, kPassCount>(row, d, p.V, c, fx, sh);
+        else if (hist)
+            f = first_pass<DT, VEC, kPassHist>(row, d, p.V, c, fx, sh);
+        else if (greedy)
+            f = first_pass<DT, VEC, kPassGreedy>(row, d, p.V, c, fx, sh);
+        else
+            f = first_pass<DT, VEC, kPassMax>(row, d, p.V, c, fx, sh);
+        f.m = block_reduce<kGivenThreads>(f.m, MaxF32(), (float*)sh.redf);
+        const int flags = block_reduce<kGivenThreads>((f.bad ? 1 : 0) | (f.over ? 2 : 0), OrI32(), (int*)sh.redf);
+        f.bad = flags & 1;
+        if (!want_hist || f.bad || (hist && !(flags & 2)) || !(f.m > -INFINITY)) break;
+        anchor = f.m;
         __syncthreads();
     }
-    bad = block_reduce<kGivenThreads>((int)bad, OrI32(), (int*)sh.redf) != 0;
-    m = uniform(m);
+    const float m = uniform(f.m);
 
     int mode = kGivenCells;
     float level = -INFINITY;  // kGivenLevel: kept iff x >= level (and finite)
-    if (bad || !(m > -INFINITY) || isnan(T) || isnan(P) || isnan(MP)) {
+    if (f.bad || !(m > -INFINITY) || isnan(T) || isnan(P) || isnan(MP)) {
         mode = kGivenError;
     } else if (greedy) {
         mode = kGivenGreedy;
@@ -364,10 +461,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
 
     if (mode == kGivenError || mode == kGivenGreedy) {
         int token = -1;
-        if (mode == kGivenGreedy) {
-            best = block_reduce<kGivenThreads>(best, MaxU64(), sh.red64);
-            token = (int)~(uint32_t)best;
-        }
+        if (mode == kGivenGreedy) token = (int)~(uint32_t)block_reduce<kGivenThreads>(f.best, MaxU64(), sh.red64);
         if (t == 0) p.out_count[b] = mode == kGivenGreedy ? 1 : 0;
         for (int64_t n = t; n < p.N; n += kGivenThreads) {
             p.out_token[b * p.N + n] = token;
@@ -380,10 +474,10 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
 
     // ---- the cells of the cuts -------------------------------------------
     double hm;  // place of the max in its cell
-    if (mode == kGivenLevel) c.base = floor((double)m * c.s) - kSlotsBelow;
+    if (mode == kGivenLevel) c.base = rint((double)m * c.s) - kSlotsBelow;
     c = uniform(c);
-    const int top = slot_of(c, m, hm);  // slot of rank 0
-    int rb = kRankNone;                 // bottom cell
+    const int top = uniform(slot_of(c, m, hm));  // slot of rank 0
+    int rb = kRankNone;                          // bottom cell
     int r_lo = 0, r_hi = -1;
     const bool cut_p = P < 1.0f;
     if (mode == kGivenCells) {
@@ -393,16 +487,18 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int r = PER * t + i, sl = top - r;
-            wt[i] = sl >= 0 && sh.hist[sl] ? rank_weight(sh.root, r) * ((double)sh.hist[sl] * inv_scale) : 0.0;
+            const uint64_t hv = sl >= 0 ? sh.hist[sl] : 0;
+            wt[i] = hv ? rank_weight(sh.root, r) * ((double)hv * inv_scale) : 0.0;
             ct[i] = sl >= 0 && use_k ? sh.cnt[sl] : 0u;
             run += wt[i];
             crun += ct[i];
         }
         double total;
         const double before = block_exclusive_sum_f64(run, sh.redf, total);
-        const uint32_t cbefore = (uint32_t)block_exclusive_sum<kGivenThreads>(crun, sh.red64);
+        uint32_t cbefore = 0, tails = 0;
         int rk = kRankNone;
         if (use_k) {
+            cbefore = (uint32_t)block_exclusive_sum<kGivenThreads>(crun, sh.red64);
             uint32_t cc = cbefore;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -410,6 +506,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 if (rk == kRankNone && cc >= (uint32_t)K && ct[i]) rk = PER * t + i;
             }
             rk = block_reduce<kGivenThreads>(rk, MinI(), (int*)sh.redf);
+            tails = (uint32_t)block_reduce<kGivenThreads>((uint64_t)f.tail, SumU64(), sh.red64);
         }
         double ht;
         // min-p's threshold is at or below the max, and may lie below the window
@@ -417,37 +514,35 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         const int rt = tmp > -INFINITY ? (int)min((int64_t)top - st, (int64_t)top + 1) : kRankNone;
         rb = min(rk, rt);
         if (cut_p && rb > top) rb = kRankNone;  // below the window: the top-p cut is above it
-        const uint32_t tails = (uint32_t)block_reduce<kGivenThreads>((uint64_t)tail, SumU64(), sh.red64);
         if (t == kGivenThreads - 1) {
             sh.n_window = cbefore + crun;
-            sh.n_above = cbefore + crun;
-            sh.s_above = total;
-            sh.w_bottom = 0.0;
+            if (rb > top) {
+                sh.n_above = cbefore + crun;
+                sh.s_above = total;
+                sh.w_bottom = 0.0;
+            }
         }
-        __syncthreads();
         if (rb <= top) {
             const int o = rb - PER * t;
             if (o >= 0 && o < PER) {
-                double ab = before;
+                double ab = before, wb = 0.0;
                 uint32_t ca = cbefore;
 #pragma unroll
-                for (int i = 0; i < PER; ++i)
+                for (int i = 0; i < PER; ++i) {
                     if (i < o) {
                         ab += wt[i];
                         ca += ct[i];
                     }
-                double wb = 0.0;
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
                     if (i == o) wb = wt[i];
+                }
                 sh.s_above = ab;
                 sh.n_above = ca;
                 sh.w_bottom = wb;
             }
-        } else if (rb == kRankNone && use_k && !cut_p && (uint64_t)sh.n_window + tails > (uint64_t)K) {
-            rb = top + 1;  // top-k cuts among the tokens below the window: they are listed as one cell
         }
         __syncthreads();
+        if (rb == kRankNone && use_k && !cut_p && (uint64_t)sh.n_window + tails > (uint64_t)K)
+            rb = top + 1;  // top-k cuts among the tokens below the window: they are listed as one cell
         if (cut_p) {
             const double lo = (double)P * sh.s_above, hi = (double)P * (sh.s_above + sh.w_bottom);
             int first_lo = kRankNone, first_hi = kRankNone, last = -1;
@@ -462,9 +557,20 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 }
                 ab += wt[i];
             }
-            first_lo = block_reduce<kGivenThreads>(first_lo, MinI(), (int*)sh.redf);
-            first_hi = block_reduce<kGivenThreads>(first_hi, MinI(), (int*)sh.redf);
-            last = block_reduce<kGivenThreads>(last, MaxI32(), (int*)sh.redf);
+            // One reduction for the three: ranks fit 13 bits, and a minimum is a
+            // maximum of the complement.
+            const auto pack = [](int v) { return (uint64_t)(v < 8191 ? 8191 - v : 0); };
+            const uint64_t three = block_reduce<kGivenThreads>(
+                pack(first_lo) << 40 | pack(first_hi) << 20 | (uint64_t)(last + 1),
+                [](uint64_t a, uint64_t e) {
+                    const uint64_t k0 = 0xFFFFFull, k1 = k0 << 20, k2 = k0 << 40;
+                    return ((a & k2) > (e & k2) ? a & k2 : e & k2) | ((a & k1) > (e & k1) ? a & k1 : e & k1) |
+                           ((a & k0) > (e & k0) ? a & k0 : e & k0);
+                },
+                sh.red64);
+            first_lo = (three >> 40) ? 8191 - (int)(three >> 40) : kRankNone;
+            first_hi = (three >> 20 & 0xFFFFF) ? 8191 - (int)(three >> 20 & 0xFFFFF) : kRankNone;
+            last = (int)(three & 0xFFFFF) - 1;
             const int end = rb <= top ? rb : last;  // where rounding leaves none above
             r_lo = min(first_lo, end);
             r_hi = min(first_hi, end);
@@ -490,51 +596,85 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         const int sl = slot_of(c, x, h);
         return sl >= 0 ? top - sl : top + 1;
     };
-    // The rank that its weight goes by (no limit at the window's end).
-    auto weight_of = [&](float x) {
-#pragma clang fp contract(off)
-        double h;
-        const int sl = slot_of(c, x, h);
+    // The weight of slot `sl`, however far down, at place h.
+    auto weight_at = [&](int sl, double h) {
         const int64_t r = (int64_t)top - sl;
         return rank_weight(sh.root, (int)min(r, (int64_t)kRankZero)) * in_cell(h);
     };
+    auto weight_of = [&](float x) {
+        double h;
+        const int sl = slot_of(c, x, h);
+        return weight_at(sl, h);
+    };
+    // A logit below every one that may be kept (a cell and a half of slack
+    // covers the roundings).
+    float floor_x = level;
+    if (mode == kGivenCells) {
+        const int r_end = rb == kRankNone ? r_hi : max(r_hi, rb);  // the last rank that may be kept
+        floor_x = -INFINITY;
+        if (r_end != kRankNone && r_end <= top && c.s > 0.0) {
+            floor_x = (float)((c.base + (double)top - (double)r_end - 1.5) / c.s);
+            floor_x = nextafterf(floor_x, -INFINITY);
+        }
+    }
+    floor_x = uniform(floor_x);
 
     // ---- pass 2: masses of the surely kept, list of the undecided -----------
     uint32_t count = 0;
     {
         double acc = 0.0;
-        for (uint32_t i = 0; i < d.steps; ++i) {
-            const uint32_t g = g_wave + i * kWave + lane;
-            if (g < d.groups) {
-                float x[GN];
-                load_group<DT>(p, row, g, x);
+        uint32_t seg_left = d.sps, seg = (uint32_t)w * d.spw;
+        stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t g, const float (&x)[GN]) {
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < GN; ++j) any |= x[j] >= floor_x && x[j] > -INFINITY;
+            if (__ballot(any)) {  // uniform: most steps of most rows hold no such token
+                uint32_t mine = 0;  // undecided tokens of this group
 #pragma unroll
                 for (int j = 0; j < GN; ++j) {
-                    if (!(x[j] > -INFINITY)) continue;
+                    const bool in = x[j] >= floor_x && x[j] > -INFINITY;
                     if (mode == kGivenLevel) {
-                        if (x[j] >= level) {
+                        if (in) {
                             acc += weight_of(x[j]);
                             ++count;
                         }
-                    } else {
+                    } else if (in) {
                         double h;
-                        const int r = rank_of(x[j], h);
+                        const int sl = slot_of(c, x[j], h);
+                        const int r = sl >= 0 ? top - sl : top + 1;
                         if (r < r_lo) {
-                            acc += weight_of(x[j]);
+                            acc += weight_at(sl, h);
                             ++count;
                         } else if (r <= r_hi || r == rb) {
-                            const uint32_t at = atomicAdd(&sh.list_n, 1u);
-                            if (at < kGivenCap) sh.list[at] = make_uint2(order_key(x[j]), g * GN + j);
+                            mine |= 1u << j;
                         }
                     }
                 }
+                // One LDS atomic reserves the wave's places in the list.
+                const uint64_t have = __ballot(mine != 0);
+                if (have) {
+                    uint32_t all;
+                    const uint32_t n = (uint32_t)__builtin_popcount(mine);
+                    const uint32_t upto = wave_inclusive_sum(n, all);
+                    uint32_t at = 0;
+                    if (lane == 0) at = atomicAdd(&sh.list_n, all);
+                    at = uniform(at) + upto - n;
+#pragma unroll
+                    for (int j = 0; j < GN; ++j)
+                        if (mine >> j & 1) {
+                            if (at < kGivenCap) sh.list[at] = make_uint2(order_key(x[j]), g * GN + j);
+                            ++at;
+                        }
+                }
             }
-            if ((i + 1) % d.sps == 0 || i + 1 == d.steps) {
+            if (--seg_left == 0 || i + 1 == d.steps) {
                 const double sum = wave_reduce(acc, [](double a, double e) { return a + e; });
-                if (lane == 0) sh.sub[w * d.spw + i / d.sps] = sum;
+                if (lane == 0) sh.sub[seg] = sum;
                 acc = 0.0;
+                ++seg;
+                seg_left = d.sps;
             }
-        }
+        });
     }
     __syncthreads();
 
@@ -553,20 +693,21 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                     fn(e.x, e.y, r, h);
                 }
             } else {
-                for (uint32_t i = 0; i < d.steps; ++i) {
-                    const uint32_t g = g_wave + i * kWave + lane;
-                    if (g >= d.groups) break;
-                    float x[GN];
-                    load_group<DT>(p, row, g, x);
-#pragma unroll
+                stream_row<DT, VEC>(row, d, p.V, [&](uint32_t, uint32_t g, const float (&x)[GN]) {
+#pragma unroll 1
                     for (int j = 0; j < GN; ++j) {
-                        if (!(x[j] > -INFINITY)) continue;
+                        if (!(x[j] >= floor_x && x[j] > -INFINITY)) continue;
                         double h;
                         const int r = rank_of(x[j], h);
                         if (r >= r_lo && (r <= r_hi || r == rb)) fn(order_key(x[j]), g * GN + j, r, h);
                     }
-                }
+                });
             }
+        };
+        // Keys that bound those of rank r's cell (a tenth of a cell to spare).
+        auto key_at = [&](int r, double off) {
+            if (!(c.s > 0.0) || r > top) return off < 0.0 ? 0u : 0xFFFFFFFFu;
+            return order_key((float)((c.base + (double)(top - r) + off) / c.s));
         };
         // The bottom cell: min-p's threshold, then the k-th largest.
         uint32_t bottom = tmp > -INFINITY ? order_key(tmp) : order_key(-3.402823466e38f);
@@ -581,17 +722,17 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                             if (rank == rb && key >= from_minp) fn(key, (uint64_t)1);
                         });
                     },
-                    [&](uint64_t) { return need; }, sh.sel);
+                    [&](uint64_t) { return need; }, sh.sel, key_at(rb, -0.6), key_at(rb, 0.6));
                 if (r.total) bottom = max(bottom, r.level);
                 __syncthreads();
             }
             if (rb <= top) {
-                uint64_t fx = 0;
+                uint64_t sum = 0;
                 undecided([&](uint32_t key, uint32_t, int rank, double h) {
-                    if (rank == rb && key >= bottom) fx += fixed_point(in_cell(h), scale);
+                    if (rank == rb && key >= bottom) sum += fx(h);
                 });
-                fx = block_reduce<kGivenThreads>(fx, SumU64(), sh.red64);
-                s_bottom = rank_weight(sh.root, rb) * ((double)fx * inv_scale);
+                sum = block_reduce<kGivenThreads>(sum, SumU64(), sh.red64);
+                s_bottom = rank_weight(sh.root, rb) * ((double)sum * inv_scale);
             }
         }
         cut = bottom;
@@ -600,8 +741,8 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 // The crossing cell: the first whose running mass reaches p S.
                 const double thr = (double)P * (sh.s_above + s_bottom);
                 double a = sh.a_lo, at = sh.a_lo;
-                int r = r_lo, found = r_lo;
-                for (; r <= r_hi; ++r) {
+                int found = r_lo;
+                for (int r = r_lo; r <= r_hi; ++r) {
                     const uint64_t hr = sh.hist[top - r];
                     const double wr = r == rb ? s_bottom : rank_weight(sh.root, r) * ((double)hr * inv_scale);
                     if (wr > 0.0) {
@@ -621,10 +762,10 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
             const SelectResult r = select_level<kGivenThreads>(
                 [&](auto fn) {
                     undecided([&](uint32_t key, uint32_t, int rank, double h) {
-                        if (rank == cp && key >= bottom) fn(key, fixed_point(in_cell(h), scale));
+                        if (rank == cp && key >= bottom) fn(key, fx(h));
                     });
                 },
-                [&](uint64_t) { return tc; }, sh.sel);
+                [&](uint64_t) { return tc; }, sh.sel, key_at(cp, -0.6), key_at(cp, 0.6));
             cut = max(bottom, r.level);
         }
         // The kept among them, added to their segments.
@@ -632,7 +773,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
             if (key >= cut) {
                 const uint32_t g = idx / GN, own = g / (d.steps * kWave), step = (g - own * d.steps * kWave) / kWave;
                 atomicAdd((unsigned long long*)&sh.subc[own * d.spw + step / d.sps],
-                          (unsigned long long)fixed_point(weight_of(key_value(key)), scale));
+                          (unsigned long long)fixed_point(weight_of(key_value(key)) * scale));
                 ++count;
             }
         });
@@ -646,7 +787,6 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
     const double mine = t < (int)subs ? sh.sub[t] + (double)sh.subc[t] * inv_scale : 0.0;
     double S;
     const double prefix = block_exclusive_sum_f64(mine, sh.redf, S);
-    __syncthreads();
     if (t < (int)subs) {
         sh.sub[t] = mine > 0.0 ? prefix + mine : -1.0;
         sh.pre[t] = prefix;
@@ -654,7 +794,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
     __syncthreads();
     if (t == 0) p.out_count[b] = (int32_t)count;
     // ln of the kept mass measured from the max itself.
-    const double ln_mass = log(S) - hm * (0.69314718055994530942 / 16.0);
+    const double ln_mass = log(S) - hm * (kLn2 / kOctave);
     for (int64_t n = w; n < p.N; n += kGivenWaves) {
         const double u = p.u_f64 ? ((const double*)p.uniforms)[b * p.N + n] : (double)((const float*)p.uniforms)[b * p.N + n];
         int token = -1;
@@ -674,45 +814,51 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 }
             }
             double run = sh.pre[lo];
-            const uint32_t own = lo / d.spw, s0 = (lo - own * d.spw) * d.sps;
+            const uint32_t own = lo / d.spw, s0 = (lo - own * d.spw) * d.sps, s1 = min(s0 + d.sps, d.steps);
             int last = -1;
-            for (uint32_t i = s0; i < min(s0 + d.sps, d.steps); ++i) {
-                const uint32_t g = (own * d.steps + i) * kWave + lane;
-                double wg[GN], sum = 0.0;
-                int mine_last = -1;
-                float x[GN];
-                if (g < d.groups) {
-                    load_group<DT>(p, row, g, x);
-                } else {
+            for (uint32_t i0 = s0; i0 < s1 && token < 0; i0 += (VEC ? kSubSteps : 2)) {
+                constexpr int AT = VEC ? kSubSteps : 2;
+                u32x4 raw[AT];
 #pragma unroll
-                    for (int j = 0; j < GN; ++j) x[j] = -INFINITY;
-                }
+                for (int k = 0; k < AT; ++k)
+                    raw[k] = load_raw<DT, VEC>(row, (own * d.steps + min(i0 + k, s1 - 1)) * kWave + lane, d.groups, p.V);
 #pragma unroll
-                for (int j = 0; j < GN; ++j) {
-                    const bool kept = x[j] > -INFINITY && x[j] >= low;
-                    wg[j] = kept ? weight_of(x[j]) : 0.0;
-                    sum += wg[j];
-                    if (wg[j] > 0.0) mine_last = (int)(g * GN + j);
-                }
-                double all;
-                const double inc = wave_inclusive_sum(sum, all);
-                const double prev = wave_shift_up1(inc);
-                const uint64_t hit = __ballot(run + inc > at);
-                if (hit) {
-                    const int L = (int)__builtin_ctzll(hit);
-                    double a = run + (lane ? prev : 0.0);
-                    int tok = -1;
+                for (int k = 0; k < AT; ++k) {
+                    if (i0 + k >= s1 || token >= 0) break;  // uniform
+                    const uint32_t g = (own * d.steps + i0 + k) * kWave + lane;
+                    float x[GN];
+                    tokens_of<DT>(raw[k], g, true, p.V, x);
+                    bool any = false;
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) any |= x[j] > -INFINITY && x[j] >= low;
+                    if (!__ballot(any)) continue;
+                    double wg[GN], sum = 0.0;
+                    int mine_last = -1;
 #pragma unroll
                     for (int j = 0; j < GN; ++j) {
-                        a += wg[j];
-                        if (tok < 0 && a > at && wg[j] > 0.0) tok = (int)(g * GN + j);
+                        const bool kept = x[j] > -INFINITY && x[j] >= low;
+                        wg[j] = kept ? weight_of(x[j]) : 0.0;
+                        sum += wg[j];
+                        if (wg[j] > 0.0) mine_last = (int)(g * GN + j);
                     }
-                    if (tok < 0) tok = mine_last;
-                    token = __builtin_amdgcn_readlane(tok, L);
-                    if (token >= 0) break;
+                    double all;
+                    const double inc = wave_inclusive_sum(sum, all);
+                    const double prev = wave_shift_up1(inc);
+                    const uint64_t hit = __ballot(run + inc > at);
+                    if (hit) {
+                        double a = run + (lane ? prev : 0.0);
+                        int tok = -1;
+#pragma unroll
+                        for (int j = 0; j < GN; ++j) {
+                            a += wg[j];
+                            if (tok < 0 && a > at && wg[j] > 0.0) tok = (int)(g * GN + j);
+                        }
+                        if (tok < 0) tok = mine_last;
+                        token = __builtin_amdgcn_readlane(tok, (int)__builtin_ctzll(hit));
+                    }
+                    run += all;
+                    last = max(last, wave_reduce(mine_last, MaxI32()));
                 }
-                run += all;
-                last = max(last, wave_reduce(mine_last, MaxI32()));
             }
             if (token < 0) token = last;
         }
@@ -732,12 +878,19 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         const double inv = 1.0 / S;
         float* out = p.out_probs + b * p.V;
         const bool vec = p.V % 4 == 0 && (uintptr_t)p.out_probs % 16 == 0;
-        for (uint32_t g = t; g < d.groups; g += kGivenThreads) {
-            float x[GN], q[GN];
-            load_group<DT>(p, row, g, x);
+        stream_row<DT, VEC>(row, d, p.V, [&](uint32_t, uint32_t g, const float (&x)[GN]) {
+            float q[GN];
+            bool any = false;
 #pragma unroll
-            for (int j = 0; j < GN; ++j)
-                q[j] = x[j] > -INFINITY && x[j] >= low ? (float)(weight_of(x[j]) * inv) : 0.0f;
+            for (int j = 0; j < GN; ++j) {
+                q[j] = 0.0f;
+                any |= x[j] > -INFINITY && x[j] >= low;
+            }
+            if (__ballot(any)) {
+#pragma unroll
+                for (int j = 0; j < GN; ++j)
+                    if (x[j] > -INFINITY && x[j] >= low) q[j] = (float)(weight_of(x[j]) * inv);
+            }
             const int64_t i0 = (int64_t)g * GN;
             if (vec && i0 + GN <= p.V) {
 #pragma unroll
@@ -747,7 +900,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 for (int j = 0; j < GN; ++j)
                     if (i0 + j < p.V) out[i0 + j] = q[j];
             }
-        }
+        });
     }
 }
 

@@ -62,18 +62,25 @@ extern "C" int nucleus_sample_given(const void* logits, int64_t B, int64_t V, co
     p.out_count = out_keep_count;
     p.out_logprob = out_token_logprob;
     p.out_probs = out_probs;
-    p.vec = (uintptr_t)logits % 16 == 0 && ((size_t)stride * esz) % 16 == 0;
+    // 16-byte loads: rows start on 16-byte boundaries and are whole groups.
+    const bool vec = (uintptr_t)logits % 16 == 0 && ((size_t)stride * esz) % 16 == 0 && ((size_t)V * esz) % 16 == 0;
     int log2v = 0;
     while ((int64_t(1) << log2v) < V) ++log2v;
     p.bits = 62 - log2v < 50 ? 62 - log2v : 50;
     hipStream_t s = (hipStream_t)o.stream;
     const dim3 grid((unsigned)B), block(kGivenThreads);
-    if (o.dtype == NUCLEUS_F32)
-        hipLaunchKernelGGL(given_row_kernel<kF32>, grid, block, 0, s, p);
+    if (o.dtype == NUCLEUS_F32 && vec)
+        hipLaunchKernelGGL((given_row_kernel<kF32, true>), grid, block, 0, s, p);
+    else if (o.dtype == NUCLEUS_F32)
+        hipLaunchKernelGGL((given_row_kernel<kF32, false>), grid, block, 0, s, p);
+    else if (o.dtype == NUCLEUS_BF16 && vec)
+        hipLaunchKernelGGL((given_row_kernel<kBF16, true>), grid, block, 0, s, p);
     else if (o.dtype == NUCLEUS_BF16)
-        hipLaunchKernelGGL(given_row_kernel<kBF16>, grid, block, 0, s, p);
+        hipLaunchKernelGGL((given_row_kernel<kBF16, false>), grid, block, 0, s, p);
+    else if (vec)
+        hipLaunchKernelGGL((given_row_kernel<kF16, true>), grid, block, 0, s, p);
     else
-        hipLaunchKernelGGL(given_row_kernel<kF16>, grid, block, 0, s, p);
+        hipLaunchKernelGGL((given_row_kernel<kF16, false>), grid, block, 0, s, p);
     return hipGetLastError() == hipSuccess ? NUCLEUS_OK : NUCLEUS_ELAUNCH;
 }
 
