@@ -10,8 +10,9 @@
 // are carried to about 1e-13 (doubles and 45-bit integers), not to the 1e-7
 // that the race needs.
 //
-// Weights.  y = x s with s = 32 log2(e) / T: a cell a = rint(y) spans a
-// thirty-second of an octave of weight, and a token of cell a weighs
+// Weights.  y = (x - x0) s with s = 32 log2(e) / T and x0 the max of the
+// first tokens loaded, the anchor: a cell a = rint(y) spans a thirty-second of
+// an octave of weight, and a token of cell a weighs
 //
 //     2^(a/32) * 2^(h/32),   h = y - a in [-1/2, 1/2],
 //
@@ -19,8 +20,8 @@
 // Cells do not move with the row max, so one pass finds the max and
 // histograms the row.  A histogram slot sums the second factors as integers of
 // `bits` fractional bits (62 - ceil(log2 V), at most 50): exact in any order.
-// The window holds 2048 cells (64 octaves) below the max of the first tokens
-// loaded and 2048 above it; what is further down weighs less than 2^-64 of the
+// The window holds 2048 cells (64 octaves) below the anchor and 2048 above
+// it; what is further down weighs less than 2^-64 of the
 // max each and is counted only.  A row whose max lies above the window takes
 // the pass again.
 //
@@ -51,9 +52,9 @@ constexpr int kSlots = 4096;      // histogram window
 constexpr int kSlotsBelow = 2048; // of it, below the anchor: 64 octaves
 constexpr int kGivenCap = 8192;   // listed tokens of undecided cells
 constexpr int kSubs = 1024;       // index segments, at most
-constexpr int kSubSteps = 8;      // steps of a segment, at least
+constexpr int kSubSteps = 4;      // steps of a segment, at least
 constexpr int kRankNone = 0x7FFFFFFF;
-constexpr int kRankZero = 1 << 16;  // a rank whose weight is 0 in double (2^-2048)
+constexpr int kFarDown = -(1 << 17); // a slot whose weight is 0 in double
 constexpr double kLn2 = 0.69314718055994530942;
 
 struct GivenParams {
@@ -85,21 +86,20 @@ __device__ constexpr double kRoot[kOctave] = {
 
 // The row's lattice.
 struct Cells {
-    double s;     // cells per logit unit; 0 for T = +inf
-    double base;  // cell of slot 0
+    double s;   // cells per logit unit
+    double x0;  // the anchor: its slot is kSlotsBelow
 };
 
-__device__ __forceinline__ Cells uniform(const Cells& c) { return Cells{uniform(c.s), uniform(c.base)}; }
+__device__ __forceinline__ Cells uniform(const Cells& c) { return Cells{uniform(c.s), uniform(c.x0)}; }
 
-// Slot of a finite logit (far below the window: negative; above: >= kSlots;
-// saturated to int32) and its place h in its cell.
+// Slot of a logit (far below the window, and for -inf: negative; above:
+// >= kSlots; saturated to int32) and its place h in its cell.  Monotone in x.
 __device__ __forceinline__ int slot_of(const Cells& c, float x, double& h)
 {
-#pragma clang fp contract(off)
-    const double y = (double)x * c.s;
+    const double y = fma((double)x - c.x0, c.s, (double)kSlotsBelow);
     const double a = rint(y);
     h = y - a;
-    return cvt_i32_sat(a - c.base);
+    return cvt_i32_sat(a);
 }
 
 // 2^(h/32) for |h| <= 1/2: Taylor's polynomial of degree 5 with its last term
@@ -137,11 +137,10 @@ __device__ __forceinline__ uint64_t fixed_point(double v)
     return (uint64_t)__double_as_longlong(v + 0x1p52) - 0x4330000000000000ull;
 }
 
-// 2^(-rank/32) for 0 <= rank; root: kRoot in LDS.
+// 2^(-rank/32); root: kRoot in LDS.  0 past about 34000 cells down.
 __device__ __forceinline__ double rank_weight(const double* root, int rank)
 {
-    const int r = -min(rank, kRankZero);
-    return ldexp(root[r & (kOctave - 1)], r >> 5);
+    return ldexp(root[-rank & (kOctave - 1)], -rank >> 5);
 }
 
 // A group: the 16 bytes of a row that a lane loads at a time.
@@ -235,47 +234,47 @@ __device__ __forceinline__ Deal deal_out(int64_t V)
 }
 
 // fn(step, group, tokens) over the wave's steps, in order, with the loads of
-// the next kAhead steps in flight (of two where they are made element by
-// element).  Every lane takes every step (past the row's end with tokens of
-// -inf).
+// the next steps (16 tokens of a lane) in flight.  Every lane takes every step
+// (past the row's end with tokens of -inf).
 template <int DT, bool VEC, class Fn>
 __device__ __forceinline__ void stream_row(const void* row, const Deal& d, int64_t V, Fn fn)
 {
-    constexpr int kAhead = VEC ? 4 : 2;
+    constexpr int GN = Group<DT>::N, AT = VEC ? 16 / GN : 1;
     const uint32_t lane = threadIdx.x & (kWave - 1), g0 = (threadIdx.x / kWave) * d.steps * kWave + lane;
-    u32x4 a[kAhead], b[kAhead];
-    auto fetch = [&](u32x4 (&to)[kAhead], uint32_t i) {
+    u32x4 a[AT], b[AT];
+    auto fetch = [&](u32x4 (&to)[AT], uint32_t i) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
+        for (int k = 0; k < AT; ++k)
             to[k] = load_raw<DT, VEC>(row, g0 + min(i + k, d.steps - 1) * kWave, d.groups, V);
     };
-    auto take = [&](const u32x4 (&from)[kAhead], uint32_t i) {
+    fetch(a, 0);
+#pragma unroll 1
+    for (uint32_t i = 0; i < d.steps; i += AT) {
+        fetch(b, i + AT);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (i + k >= d.steps) return;  // uniform
+        for (int k = 0; k < AT; ++k) {
             const uint32_t g = g0 + (i + k) * kWave;
-            float x[Group<DT>::N];
-            tokens_of<DT>(from[k], g, uniform((int)((int64_t)(g - lane + kWave) * Group<DT>::N > V)) != 0, V, x);
+            float x[GN];
+            // Steps past the wave's last read tokens of the next wave: -inf.
+            const bool edge = uniform((int)(i + k >= d.steps || (int64_t)(g - lane + kWave) * GN > V)) != 0;
+            tokens_of<DT>(a[k], g, edge, i + k < d.steps ? V : 0, x);
             fn(i + k, g, x);
         }
-    };
-    fetch(a, 0);
-    for (uint32_t i = 0; i < d.steps; i += 2 * kAhead) {
-        fetch(b, i + kAhead);
-        take(a, i);
-        if (i + kAhead >= d.steps) break;
-        fetch(a, i + 2 * kAhead);
-        take(b, i + kAhead);
+#pragma unroll
+        for (int k = 0; k < AT; ++k) a[k] = b[k];
     }
 }
 
 struct GivenShared {
-    uint64_t hist[kSlots];
+    // Integer masses of the cells; from the second pass on, the slots of the
+    // surely kept cells hold their 2^(-rank/32) as doubles instead, and the last
+    // one 0.
+    uint64_t hist[kSlots + 1];
     uint32_t cnt[kSlots];
-    uint2 list[kGivenCap];     // key, index
+    uint2 list[kGivenCap];     // logit, index
     double sub[kSubs];         // mass of each segment's surely kept tokens; then of the segments up to it (-1: empty)
     uint64_t subc[kSubs];      // mass of its kept listed tokens, at 2^-bits
-    double pre[kSubs];         // mass of the segments before it
+    double pre[kSubs];         // number of its undecided tokens; then mass of the segments before it
     double root[kOctave];
     SelectShared sel;
     uint64_t red64[kGivenWaves];
@@ -288,6 +287,7 @@ struct GivenShared {
     uint64_t tc;
 };
 
+struct SumF64 { __device__ double operator()(double a, double b) const { return a + b; } };
 struct MinI { __device__ int operator()(int a, int b) const { return a < b ? a : b; } };
 struct MaxF32 { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 
@@ -320,40 +320,41 @@ enum : int {
     kGivenCells = 3,   // kept: by cells and the listed tokens
 };
 
-// What the first pass finds.
+// What the first pass finds (each thread its own).
 struct FirstPass {
-    float m;         // max
-    bool bad;        // NaN or +inf seen (this thread)
-    bool over;       // a token above the window (this thread)
-    uint32_t tail;   // finite tokens below the window (this thread)
-    uint64_t best;   // greedy: (key, ~index) of this thread's max
+    float m;         // max; NaN or +inf if one was seen
+    uint32_t at;     // without a histogram: the step that first held it
+    bool over;       // a token above the window
+    uint32_t tail;   // for top-k rows: finite tokens below the window
 };
 
-enum : int { kPassMax = 0, kPassGreedy = 1, kPassHist = 2, kPassCount = 3 };
-
-template <int DT, bool VEC, int PASS>
+template <int DT, bool VEC, bool HIST>
 __device__ __forceinline__ FirstPass first_pass(const void* row, const Deal& d, int64_t V, const Cells& c,
-                                                const Fixed& fx, GivenShared& sh)
+                                                const Fixed& fx, bool use_k, GivenShared& sh)
 {
-    FirstPass r = {-INFINITY, false, false, 0, 0};
-    stream_row<DT, VEC>(row, d, V, [&](uint32_t, uint32_t g, const float (&x)[Group<DT>::N]) {
+    constexpr int GN = Group<DT>::N;
+    FirstPass r = {-INFINITY, 0, false, 0};
+    stream_row<DT, VEC>(row, d, V, [&](uint32_t i, uint32_t, const float (&x)[GN]) {
+        float most = x[0];  // IEEE maximum: NaN stays
 #pragma unroll
-        for (int j = 0; j < Group<DT>::N; ++j) {
-            r.bad |= !(x[j] < INFINITY);
-            r.m = fmaxf(r.m, x[j]);
-            if constexpr (PASS == kPassGreedy) {
-                const uint64_t pk = ((uint64_t)order_key(x[j]) << 32) | (uint32_t)~(uint32_t)(g * Group<DT>::N + j);
-                r.best = pk > r.best ? pk : r.best;
-            }
-            if constexpr (PASS >= kPassHist) {
+        for (int j = 1; j < GN; ++j) most = __builtin_elementwise_maximum(most, x[j]);
+        if constexpr (!HIST) {
+            if (!(most <= r.m)) r.at = i;
+        }
+        r.m = __builtin_elementwise_maximum(r.m, most);
+        if constexpr (HIST) {
+#pragma unroll
+            for (int j = 0; j < GN; ++j) {
                 double h;
                 const int sl = slot_of(c, x[j], h);
-                if ((uint32_t)sl < (uint32_t)kSlots && x[j] > -INFINITY) {
-                    atomicAdd((unsigned long long*)&sh.hist[sl], (unsigned long long)fx(h));
-                    if constexpr (PASS == kPassCount) atomicAdd(&sh.cnt[sl], 1u);
-                } else {
-                    r.over |= sl >= kSlots;
-                    if constexpr (PASS == kPassCount) r.tail += x[j] > -INFINITY;
+                const uint64_t q = fx(h);
+                if ((uint32_t)sl < (uint32_t)kSlots) {
+                    atomicAdd((unsigned long long*)&sh.hist[sl], (unsigned long long)q);
+                    if (use_k) atomicAdd(&sh.cnt[sl], 1u);
+                } else if (sl >= kSlots) {
+                    r.over = true;
+                } else if (use_k) {
+                    r.tail += x[j] > -INFINITY;
                 }
             }
         }
@@ -374,25 +375,26 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
     const double scale = ldexp(1.0, p.bits), inv_scale = ldexp(1.0, -p.bits);
     const Fixed fx(scale);
 
-    const float T = p.temperature[b], P = p.top_p[b];
-    const int K = p.top_k ? p.top_k[b] : 0;
-    const float MP = p.min_p ? p.min_p[b] : 0.0f;
+    const float T = uniform(p.temperature[b]), P = uniform(p.top_p[b]);
+    const int K = p.top_k ? uniform(p.top_k[b]) : 0;
+    const float MP = p.min_p ? uniform(p.min_p[b]) : 0.0f;
     const bool greedy = T <= 0.0f;
     const bool use_k = K > 0 && (int64_t)K < p.V;
     // A histogram is needed where a cut has to be searched for.
     const bool want_hist = !greedy && P > 0.0f && (P < 1.0f || use_k);
 
     if (t < kOctave) sh.root[t] = kRoot[t];
-    for (int i = t; i < kSubs; i += kGivenThreads) {
-        sh.sub[i] = 0.0;
-        sh.subc[i] = 0;
-    }
+    static_assert(kSubs == kGivenThreads, "one segment per thread");
+    sh.sub[t] = 0.0;
+    sh.pre[t] = 0.0;
+    sh.subc[t] = 0;
     if (t == 0) sh.list_n = 0;
 
     // ---- pass 1: max, NaN / +inf, histogram -----------------------------
     Cells c;
-    c.s = (greedy || T == INFINITY) ? 0.0 : (kOctave * 1.4426950408889634074) / (double)T;
-    c.base = 0.0;
+    // T = +inf: cells wider than any logit, so that every weight is 1.
+    c.s = T == INFINITY ? 0x1p-1000 : (kOctave * 1.4426950408889634074) / (double)T;
+    c.x0 = 0.0;
     FirstPass f;
     float anchor = -INFINITY;
     if (want_hist) {
@@ -402,66 +404,67 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
 #pragma unroll
         for (int j = 0; j < GN; ++j) anchor = fmaxf(anchor, x[j]);
-        anchor = block_reduce<kGivenThreads>(anchor, MaxF32(), (float*)sh.redf);
+        for (int i = t; i <= kSlots; i += kGivenThreads) sh.hist[i] = 0;
+        if (use_k)
+            for (int i = t; i < kSlots; i += kGivenThreads) sh.cnt[i] = 0;
+        anchor = uniform(block_reduce<kGivenThreads>(anchor, MaxF32(), (float*)sh.redf));
     }
-    // At most two attempts: the second is anchored at the row's own max.
-    for (int attempt = 0; attempt < 2; ++attempt) {
-        const bool hist = want_hist && anchor > -INFINITY && anchor < INFINITY;
+    float m = -INFINITY;
+    bool hist = want_hist && anchor > -INFINITY && anchor < INFINITY;
+    // At most three turns: for the max alone where the first tokens were all
+    // masked, with a histogram, and once more where a token lay above its window.
+#pragma unroll 1
+    for (int turn = 0; turn < 3; ++turn) {
         if (hist) {
-            c.base = rint((double)anchor * c.s) - kSlotsBelow;
-            for (int i = t; i < kSlots; i += kGivenThreads) {
-                sh.hist[i] = 0;
-                sh.cnt[i] = 0;
-            }
+            c.x0 = (double)anchor;
+            c = uniform(c);
+            f = first_pass<DT, VEC, true>(row, d, p.V, c, fx, use_k, sh);
+        } else {
+            f = first_pass<DT, VEC, false>(row, d, p.V, c, fx, use_k, sh);
+        }
+        // One reduction for the max and whether a token lay above the window
+        // (keys order NaN and +inf above every finite logit here, sign aside).
+        const uint32_t key = order_key(f.m != f.m ? INFINITY : f.m);
+        const uint64_t all = block_reduce<kGivenThreads>((uint64_t)key << 1 | (f.over ? 1 : 0),
+                                                         [](uint64_t a, uint64_t e) {
+                                                             return (a > e ? a | (e & 1) : e | (a & 1));
+                                                         }, sh.red64);
+        m = uniform(key_value((uint32_t)(all >> 1)));
+        if (!want_hist || !(m > -INFINITY && m < INFINITY) || (hist && !(all & 1))) break;
+        // Anchored at the row's own max, no token lies above the window.
+        anchor = m;
+        if (hist) {
+            for (int i = t; i <= kSlots; i += kGivenThreads) sh.hist[i] = 0;
+            if (use_k)
+                for (int i = t; i < kSlots; i += kGivenThreads) sh.cnt[i] = 0;
             __syncthreads();
         }
-        c = uniform(c);
-        if (hist && use_k)
-            f = first_pass<DT, VEC, kPassCount>(row, d, p.V, c, fx, sh);
-        else if (hist)
-            f = first_pass<DT, VEC, kPassHist>(row, d, p.V, c, fx, sh);
-        else if (greedy)
-            f = first_pass<DT, VEC, kPassGreedy>(row, d, p.V, c, fx, sh);
-        else
-            f = first_pass<DT, VEC, kPassMax>(row, d, p.V, c, fx, sh);
-        f.m = block_reduce<kGivenThreads>(f.m, MaxF32(), (float*)sh.redf);
-        const int flags = block_reduce<kGivenThreads>((f.bad ? 1 : 0) | (f.over ? 2 : 0), OrI32(), (int*)sh.redf);
-        f.bad = flags & 1;
-        if (!want_hist || f.bad || (hist && !(flags & 2)) || !(f.m > -INFINITY)) break;
-        anchor = f.m;
-        __syncthreads();
+        hist = true;
     }
-    const float m = uniform(f.m);
 
     int mode = kGivenCells;
     float level = -INFINITY;  // kGivenLevel: kept iff x >= level (and finite)
-    if (f.bad || !(m > -INFINITY) || isnan(T) || isnan(P) || isnan(MP)) {
+    if (!(m > -INFINITY && m < INFINITY) || isnan(T) || isnan(P) || isnan(MP)) {
         mode = kGivenError;
     } else if (greedy) {
         mode = kGivenGreedy;
     }
-    // min-p: w_i >= min_p w_max  <=>  x_i >= m + T ln(min_p), rounded up.
-    float tmp = -INFINITY;
-    if (mode == kGivenCells) {
-        const float mpc = MP > 1.0f ? 1.0f : MP;
-        if (mpc > 0.0f && T != INFINITY) {
-            const double td = (double)m + (double)T * log((double)mpc);
-            float tf = (float)td;
-            if ((double)tf < td) tf = nextafterf(tf, INFINITY);
-            tmp = uniform(tf);
-        }
-        if (P <= 0.0f) {
-            mode = kGivenLevel;
-            level = m;
-        } else if (!want_hist) {
-            mode = kGivenLevel;
-            level = tmp;
-        }
-    }
-
     if (mode == kGivenError || mode == kGivenGreedy) {
         int token = -1;
-        if (mode == kGivenGreedy) token = (int)~(uint32_t)block_reduce<kGivenThreads>(f.best, MaxU64(), sh.red64);
+        if (mode == kGivenGreedy) {
+            // The lowest index that holds the max: every thread knows the step
+            // that first held its own.
+            uint32_t first = 0xFFFFFFFFu;
+            if (f.m == m) {
+                const uint32_t g = ((uint32_t)w * d.steps + f.at) * kWave + lane;
+                float x[GN];
+                tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
+#pragma unroll
+                for (int j = GN - 1; j >= 0; --j)
+                    if (x[j] == m) first = g * GN + j;
+            }
+            token = (int)block_reduce<kGivenThreads>(first, MinU32(), (uint32_t*)sh.red64);
+        }
         if (t == 0) p.out_count[b] = mode == kGivenGreedy ? 1 : 0;
         for (int64_t n = t; n < p.N; n += kGivenThreads) {
             p.out_token[b * p.N + n] = token;
@@ -471,12 +474,28 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
             for (int64_t i = t; i < p.V; i += kGivenThreads) p.out_probs[b * p.V + i] = i == token ? 1.0f : 0.0f;
         return;
     }
+    // min-p: w_i >= min_p w_max  <=>  x_i >= m + T ln(min_p), rounded up.
+    float tmp = -INFINITY;
+    if (MP > 0.0f && T != INFINITY) {
+        const double td = (double)m + (double)T * log((double)fminf(MP, 1.0f));
+        float tf = (float)td;
+        if ((double)tf < td) tf = nextafterf(tf, INFINITY);
+        tmp = uniform(tf);
+    }
+    if (P <= 0.0f) {
+        mode = kGivenLevel;
+        level = m;
+    } else if (!want_hist) {
+        mode = kGivenLevel;
+        level = tmp;
+    }
 
     // ---- the cells of the cuts -------------------------------------------
     double hm;  // place of the max in its cell
-    if (mode == kGivenLevel) c.base = rint((double)m * c.s) - kSlotsBelow;
+    if (mode == kGivenLevel) c.x0 = (double)m;
     c = uniform(c);
     const int top = uniform(slot_of(c, m, hm));  // slot of rank 0
+    hm = uniform(hm);
     int rb = kRankNone;                          // bottom cell
     int r_lo = 0, r_hi = -1;
     const bool cut_p = P < 1.0f;
@@ -596,187 +615,241 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         const int sl = slot_of(c, x, h);
         return sl >= 0 ? top - sl : top + 1;
     };
-    // The weight of slot `sl`, however far down, at place h.
-    auto weight_at = [&](int sl, double h) {
-        const int64_t r = (int64_t)top - sl;
-        return rank_weight(sh.root, (int)min(r, (int64_t)kRankZero)) * in_cell(h);
-    };
+    // The weight of a finite token, however far down.
     auto weight_of = [&](float x) {
         double h;
         const int sl = slot_of(c, x, h);
-        return weight_at(sl, h);
+        return rank_weight(sh.root, top - max(sl, kFarDown)) * in_cell(h);
     };
-    // A logit below every one that may be kept (a cell and a half of slack
-    // covers the roundings).
-    float floor_x = level;
+    // A logit below every one that may be kept, and above -inf (a cell and a
+    // half of slack covers the roundings).
+    const float lowest = -3.402823466e38f;
+    float floor_x = fmaxf(level, lowest);
+    const int s_lo = r_lo > top ? -1 : top - r_lo;  // slots above it are surely kept
     if (mode == kGivenCells) {
         const int r_end = rb == kRankNone ? r_hi : max(r_hi, rb);  // the last rank that may be kept
-        floor_x = -INFINITY;
-        if (r_end != kRankNone && r_end <= top && c.s > 0.0) {
-            floor_x = (float)((c.base + (double)top - (double)r_end - 1.5) / c.s);
-            floor_x = nextafterf(floor_x, -INFINITY);
-        }
+        if (r_end <= top) floor_x = fmaxf((float)(c.x0 + ((double)(top - r_end - kSlotsBelow) - 1.5) / c.s), lowest);
+        if (floor_x > lowest) floor_x = nextafterf(floor_x, -INFINITY);
     }
     floor_x = uniform(floor_x);
 
     // ---- pass 2: masses of the surely kept, list of the undecided -----------
-    uint32_t count = 0;
+    const int s_sure = mode == kGivenLevel ? -1 : s_lo;  // tokens above floor_x in slots above it are kept
+    for (int i = s_sure + 1 + t; i <= top; i += kGivenThreads)
+        sh.hist[i] = (uint64_t)__double_as_longlong(rank_weight(sh.root, top - i));
+    if (t == 0) sh.hist[kSlots] = 0;
+    __syncthreads();
+    // Tokens above floor_x in other slots from s_und up, or in slot s_bot, are
+    // undecided; those below the window (negative slots, far up as unsigned)
+    // are looked at with them.
+    const uint32_t s_und = mode == kGivenLevel || r_hi > top ? 0u : (uint32_t)(top - r_hi);
+    const int s_bot = mode == kGivenLevel || rb > top ? kSlots : top - rb;
+    uint32_t count = 0;                     // kept tokens, of lane 0 and of each lane
+    uint32_t kmin = 0xFFFFFFFFu, kmax = 0;  // keys of the undecided that are not listed
     {
         double acc = 0.0;
-        uint32_t seg_left = d.sps, seg = (uint32_t)w * d.spw;
+        uint32_t seg_left = d.sps, seg = (uint32_t)w * d.spw, sure_n = 0, und_n = 0;
         stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t g, const float (&x)[GN]) {
-            bool any = false;
+            float most = x[0];
 #pragma unroll
-            for (int j = 0; j < GN; ++j) any |= x[j] >= floor_x && x[j] > -INFINITY;
-            if (__ballot(any)) {  // uniform: most steps of most rows hold no such token
-                uint32_t mine = 0;  // undecided tokens of this group
+            for (int j = 1; j < GN; ++j) most = fmaxf(most, x[j]);
+            if (__ballot(most >= floor_x)) {  // uniform: most steps of most rows hold no such token
+                uint64_t some[GN];  // lanes whose j-th token is undecided or below the window
+                uint32_t n = 0;
 #pragma unroll
                 for (int j = 0; j < GN; ++j) {
-                    const bool in = x[j] >= floor_x && x[j] > -INFINITY;
-                    if (mode == kGivenLevel) {
-                        if (in) {
-                            acc += weight_of(x[j]);
-                            ++count;
-                        }
-                    } else if (in) {
-                        double h;
-                        const int sl = slot_of(c, x[j], h);
-                        const int r = sl >= 0 ? top - sl : top + 1;
-                        if (r < r_lo) {
-                            acc += weight_at(sl, h);
-                            ++count;
-                        } else if (r <= r_hi || r == rb) {
-                            mine |= 1u << j;
+                    double h;  // (finite: a -inf here would make the sum NaN)
+                    const int sl = slot_of(c, fmaxf(x[j], floor_x), h);
+                    const bool in = x[j] >= floor_x, sure = in && sl > s_sure;
+                    const uint64_t e = sh.hist[sure ? sl : kSlots];
+                    acc = fma(__longlong_as_double((long long)e), in_cell(h), acc);
+                    sure_n += (uint32_t)__builtin_popcountll(__ballot(sure));
+                    some[j] = __ballot(in && !sure && ((uint32_t)sl >= s_und || sl == s_bot));
+                    n += (uint32_t)__builtin_popcountll(some[j]);
+                }
+                if (n) {  // uniform
+                    if (mode == kGivenLevel || r_lo > top) {
+                        // Tokens below the window: kept by their own weight, unless
+                        // top-k cuts among them (they are then one cell).
+#pragma unroll
+                        for (int j = 0; j < GN; ++j)
+                            if (some[j] >> lane & 1) {
+                                if (rb != top + 1) {
+                                    acc += weight_of(x[j]);
+                                    ++count;
+                                }
+                            }
+                    }
+                    if (mode == kGivenCells && r_lo != kRankNone) {
+                        // One LDS atomic reserves the wave's places in the list.
+                        und_n += n;
+                        uint32_t at = 0;
+                        if (lane == 0) at = atomicAdd(&sh.list_n, n);
+                        at = uniform(at);
+#pragma unroll
+                        for (int j = 0; j < GN; ++j) {
+                            if (some[j] >> lane & 1) {
+                                const uint32_t mine = at + __builtin_amdgcn_mbcnt_hi(
+                                    (uint32_t)(some[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some[j], 0));
+                                if (mine < kGivenCap) {
+                                    sh.list[mine] = make_uint2(__float_as_uint(x[j]), g * GN + j);
+                                } else {
+                                    const uint32_t key = order_key(x[j]);
+                                    kmin = min(kmin, key);
+                                    kmax = max(kmax, key);
+                                }
+                            }
+                            at += (uint32_t)__builtin_popcountll(some[j]);
                         }
                     }
                 }
-                // One LDS atomic reserves the wave's places in the list.
-                const uint64_t have = __ballot(mine != 0);
-                if (have) {
-                    uint32_t all;
-                    const uint32_t n = (uint32_t)__builtin_popcount(mine);
-                    const uint32_t upto = wave_inclusive_sum(n, all);
-                    uint32_t at = 0;
-                    if (lane == 0) at = atomicAdd(&sh.list_n, all);
-                    at = uniform(at) + upto - n;
-#pragma unroll
-                    for (int j = 0; j < GN; ++j)
-                        if (mine >> j & 1) {
-                            if (at < kGivenCap) sh.list[at] = make_uint2(order_key(x[j]), g * GN + j);
-                            ++at;
-                        }
-                }
             }
             if (--seg_left == 0 || i + 1 == d.steps) {
-                const double sum = wave_reduce(acc, [](double a, double e) { return a + e; });
-                if (lane == 0) sh.sub[seg] = sum;
+                const double sum = wave_reduce(acc, SumF64());
+                if (lane == 0) {
+                    sh.sub[seg] = sum;
+                    sh.pre[seg] = (double)und_n;
+                }
                 acc = 0.0;
+                und_n = 0;
                 ++seg;
                 seg_left = d.sps;
             }
         });
+        if (lane == 0) count += sure_n;
     }
     __syncthreads();
 
     // ---- the exact cut level ---------------------------------------------
-    uint32_t cut = mode == kGivenLevel ? (level > -INFINITY ? order_key(level) : order_key(-3.402823466e38f)) : 0u;
+    uint32_t cut = order_key(fmaxf(level, lowest));
+    double one_weight = 0.0;  // every undecided token is kept, with this weight
     if (mode == kGivenCells) {
         const uint32_t ln = sh.list_n;
         const bool listed = ln <= kGivenCap;
         // Every undecided token (key, index), from the list or from memory.
         auto undecided = [&](auto fn) {
-            if (listed) {
-                for (uint32_t i = t; i < ln; i += kGivenThreads) {
-                    const uint2 e = sh.list[i];
-                    double h;
-                    const int r = rank_of(key_value(e.x), h);
-                    fn(e.x, e.y, r, h);
-                }
-            } else {
-                stream_row<DT, VEC>(row, d, p.V, [&](uint32_t, uint32_t g, const float (&x)[GN]) {
+            const uint32_t n = listed ? ln : (uint32_t)p.V;
 #pragma unroll 1
-                    for (int j = 0; j < GN; ++j) {
-                        if (!(x[j] >= floor_x && x[j] > -INFINITY)) continue;
-                        double h;
-                        const int r = rank_of(x[j], h);
-                        if (r >= r_lo && (r <= r_hi || r == rb)) fn(order_key(x[j]), g * GN + j, r, h);
-                    }
-                });
+            for (uint32_t i = t; i < n; i += kGivenThreads) {
+                float x;
+                uint32_t idx = i;
+                if (listed) {
+                    x = __uint_as_float(sh.list[i].x);
+                    idx = sh.list[i].y;
+                } else {
+                    x = logit_at<DT>(row, i);
+                    if (!(x >= floor_x)) continue;
+                }
+                double h;
+                const int r = rank_of(x, h);
+                if (r >= r_lo && (r <= r_hi || r == rb)) fn(x, idx, r, h);
             }
         };
         // Keys that bound those of rank r's cell (a tenth of a cell to spare).
         auto key_at = [&](int r, double off) {
-            if (!(c.s > 0.0) || r > top) return off < 0.0 ? 0u : 0xFFFFFFFFu;
-            return order_key((float)((c.base + (double)(top - r) + off) / c.s));
+            if (r > top) return off < 0.0 ? 0u : 0xFFFFFFFFu;
+            return order_key((float)(c.x0 + ((double)(top - r - kSlotsBelow) + off) / c.s));
         };
-        // The bottom cell: min-p's threshold, then the k-th largest.
-        uint32_t bottom = tmp > -INFINITY ? order_key(tmp) : order_key(-3.402823466e38f);
-        double s_bottom = 0.0;
-        if (rb != kRankNone) {
-            const uint32_t from_minp = bottom;
-            if (use_k && sh.n_above < (uint32_t)K) {
-                const uint64_t need = (uint64_t)K - sh.n_above;
-                const SelectResult r = select_level<kGivenThreads>(
-                    [&](auto fn) {
-                        undecided([&](uint32_t key, uint32_t, int rank, double) {
-                            if (rank == rb && key >= from_minp) fn(key, (uint64_t)1);
-                        });
-                    },
-                    [&](uint64_t) { return need; }, sh.sel, key_at(rb, -0.6), key_at(rb, 0.6));
-                if (r.total) bottom = max(bottom, r.level);
-                __syncthreads();
+        // Long runs of one value (more undecided tokens than the list holds,
+        // all of one key): they share a fate, which needs no search.
+        uint32_t one_key = 0;
+        if (!listed) {
+            for (uint32_t i = t; i < kGivenCap; i += kGivenThreads) {
+                const uint32_t key = order_key(__uint_as_float(sh.list[i].x));
+                kmin = min(kmin, key);
+                kmax = max(kmax, key);
             }
-            if (rb <= top) {
+            const uint64_t both = block_reduce<kGivenThreads>(
+                (uint64_t)kmax << 32 | (uint32_t)~kmin,
+                [](uint64_t a, uint64_t e) {
+                    const uint64_t hi = 0xFFFFFFFF00000000ull;
+                    return ((a & hi) > (e & hi) ? a & hi : e & hi) | ((uint32_t)a > (uint32_t)e ? (uint32_t)a : (uint32_t)e);
+                },
+                sh.red64);
+            if ((uint32_t)(both >> 32) == ~(uint32_t)both) one_key = (uint32_t)(both >> 32);
+        }
+        const uint32_t from_minp = order_key(fmaxf(tmp, lowest));
+        uint32_t bottom = from_minp;  // lowest key that survives min-p and top-k
+        double s_bottom = 0.0;        // mass of the bottom cell's survivors
+        // First the bottom cell by top-k (each token counts 1), then the
+        // crossing cell by top-p (each token counts its weight).
+#pragma unroll 1
+        for (int step = 0; step < 2; ++step) {
+            int cell;
+            uint64_t thr;
+            if (step == 0) {
+                if (rb == kRankNone) continue;
+                cell = rb;
+                thr = use_k && sh.n_above < (uint32_t)K ? (uint64_t)K - sh.n_above : 0;
+            } else {
+                if (!cut_p) break;
+                if (t == 0) {
+                    // The crossing cell: the first whose running mass reaches p S.
+                    const double want = (double)P * (sh.s_above + s_bottom);
+                    double a = sh.a_lo, at = sh.a_lo;
+                    int found = r_lo;
+#pragma unroll 1
+                    for (int r = r_lo; r <= r_hi; ++r) {
+                        const double wr =
+                            r == rb ? s_bottom : rank_weight(sh.root, r) * ((double)sh.hist[top - r] * inv_scale);
+                        if (wr > 0.0) {
+                            found = r;
+                            at = a;
+                            if (a + wr >= want) break;
+                        }
+                        a += wr;
+                    }
+                    const double q = (want - at) / (rank_weight(sh.root, found) * inv_scale);
+                    sh.cross = found;
+                    sh.tc = !(q > 1.0) ? 1 : (q < 1.8e19 ? (uint64_t)ceil(q) : ~0ull);
+                }
+                __syncthreads();
+                cell = uniform(sh.cross);
+                thr = sh.tc;
+            }
+            if (thr) {
+                uint32_t found = one_key;
+                if (!one_key) {
+                    const SelectResult r = select_level<kGivenThreads>(
+                        [&](auto fn) {
+                            undecided([&](float x, uint32_t, int rank, double h) {
+                                const uint32_t key = order_key(x);
+                                if (rank == cell && key >= bottom) fn(key, step ? fx(h) : (uint64_t)1);
+                            });
+                        },
+                        [&](uint64_t) { return thr; }, sh.sel, key_at(cell, -0.6), key_at(cell, 0.6));
+                    found = r.total ? r.level : 0u;
+                }
+                bottom = max(bottom, found);
+            }
+            if (step == 0 && rb <= top && cut_p) {
                 uint64_t sum = 0;
-                undecided([&](uint32_t key, uint32_t, int rank, double h) {
-                    if (rank == rb && key >= bottom) sum += fx(h);
-                });
+                if (one_key) {
+                    sum = t == 0 && one_key >= bottom ? sh.hist[top - rb] : 0;
+                } else {
+                    undecided([&](float x, uint32_t, int rank, double h) {
+                        if (rank == rb && order_key(x) >= bottom) sum += fx(h);
+                    });
+                }
                 sum = block_reduce<kGivenThreads>(sum, SumU64(), sh.red64);
                 s_bottom = rank_weight(sh.root, rb) * ((double)sum * inv_scale);
             }
         }
         cut = bottom;
-        if (cut_p) {
-            if (t == 0) {
-                // The crossing cell: the first whose running mass reaches p S.
-                const double thr = (double)P * (sh.s_above + s_bottom);
-                double a = sh.a_lo, at = sh.a_lo;
-                int found = r_lo;
-                for (int r = r_lo; r <= r_hi; ++r) {
-                    const uint64_t hr = sh.hist[top - r];
-                    const double wr = r == rb ? s_bottom : rank_weight(sh.root, r) * ((double)hr * inv_scale);
-                    if (wr > 0.0) {
-                        found = r;
-                        at = a;
-                        if (a + wr >= thr) break;
-                    }
-                    a += wr;
+        if (one_key) {
+            one_weight = one_key >= cut ? weight_of(key_value(one_key)) : 0.0;
+            if (one_key >= cut && t == 0) count += ln;
+        } else {
+            // The kept among them, added to their segments.
+            undecided([&](float x, uint32_t idx, int, double) {
+                if (order_key(x) >= cut) {
+                    const uint32_t step = idx / (GN * kWave), own = step / d.steps;
+                    atomicAdd((unsigned long long*)&sh.subc[own * d.spw + (step - own * d.steps) / d.sps],
+                              (unsigned long long)fixed_point(weight_of(x) * scale));
+                    ++count;
                 }
-                const double q = (thr - at) / (rank_weight(sh.root, found) * inv_scale);
-                sh.cross = found;
-                sh.tc = !(q > 1.0) ? 1 : (q < 1.8e19 ? (uint64_t)ceil(q) : ~0ull);
-            }
-            __syncthreads();
-            const int cp = uniform(sh.cross);
-            const uint64_t tc = sh.tc;
-            const SelectResult r = select_level<kGivenThreads>(
-                [&](auto fn) {
-                    undecided([&](uint32_t key, uint32_t, int rank, double h) {
-                        if (rank == cp && key >= bottom) fn(key, fx(h));
-                    });
-                },
-                [&](uint64_t) { return tc; }, sh.sel, key_at(cp, -0.6), key_at(cp, 0.6));
-            cut = max(bottom, r.level);
+            });
         }
-        // The kept among them, added to their segments.
-        undecided([&](uint32_t key, uint32_t idx, int, double) {
-            if (key >= cut) {
-                const uint32_t g = idx / GN, own = g / (d.steps * kWave), step = (g - own * d.steps * kWave) / kWave;
-                atomicAdd((unsigned long long*)&sh.subc[own * d.spw + step / d.sps],
-                          (unsigned long long)fixed_point(weight_of(key_value(key)) * scale));
-                ++count;
-            }
-        });
         __syncthreads();
     }
     const float low = key_value(cut);  // kept: finite and x >= low
@@ -784,13 +857,11 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
     // ---- the draws ---------------------------------------------------------
     count = (uint32_t)block_reduce<kGivenThreads>((uint64_t)count, SumU64(), sh.red64);
     const uint32_t subs = d.spw * kGivenWaves;
-    const double mine = t < (int)subs ? sh.sub[t] + (double)sh.subc[t] * inv_scale : 0.0;
+    const double mine = sh.sub[t] + one_weight * sh.pre[t] + (double)sh.subc[t] * inv_scale;
     double S;
     const double prefix = block_exclusive_sum_f64(mine, sh.redf, S);
-    if (t < (int)subs) {
-        sh.sub[t] = mine > 0.0 ? prefix + mine : -1.0;
-        sh.pre[t] = prefix;
-    }
+    sh.sub[t] = mine > 0.0 ? prefix + mine : -1.0;
+    sh.pre[t] = prefix;
     __syncthreads();
     if (t == 0) p.out_count[b] = (int32_t)count;
     // ln of the kept mass measured from the max itself.
@@ -804,7 +875,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
             uint32_t lo = 0;
             bool found = false;
             for (uint32_t i = 0; i < subs && !found; i += kWave) {
-                const double v = i + lane < subs ? sh.sub[i + lane] : -1.0;
+                const double v = sh.sub[i + lane];
                 const uint64_t over = __ballot(v > at), any = __ballot(v >= 0.0);
                 if (over) {
                     lo = i + (uint32_t)__builtin_ctzll(over);
@@ -814,51 +885,48 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 }
             }
             double run = sh.pre[lo];
-            const uint32_t own = lo / d.spw, s0 = (lo - own * d.spw) * d.sps, s1 = min(s0 + d.sps, d.steps);
+            const uint32_t own = lo / d.spw, s0 = own * d.steps + (lo - own * d.spw) * d.sps;
+            const uint32_t s1 = min(s0 + d.sps, (own + 1) * d.steps);
             int last = -1;
-            for (uint32_t i0 = s0; i0 < s1 && token < 0; i0 += (VEC ? kSubSteps : 2)) {
-                constexpr int AT = VEC ? kSubSteps : 2;
-                u32x4 raw[AT];
+            u32x4 raw[kSubSteps];
 #pragma unroll
-                for (int k = 0; k < AT; ++k)
-                    raw[k] = load_raw<DT, VEC>(row, (own * d.steps + min(i0 + k, s1 - 1)) * kWave + lane, d.groups, p.V);
+            for (int k = 0; k < kSubSteps; ++k)
+                raw[k] = load_raw<DT, VEC>(row, min(s0 + k, s1 - 1) * kWave + lane, d.groups, p.V);
+#pragma unroll 1
+            for (uint32_t i = s0; i < s1 && token < 0; ++i) {
+                const uint32_t g = i * kWave + lane;
+                float x[GN];
+                tokens_of<DT>(raw[0], g, true, p.V, x);
 #pragma unroll
-                for (int k = 0; k < AT; ++k) {
-                    if (i0 + k >= s1 || token >= 0) break;  // uniform
-                    const uint32_t g = (own * d.steps + i0 + k) * kWave + lane;
-                    float x[GN];
-                    tokens_of<DT>(raw[k], g, true, p.V, x);
-                    bool any = false;
+                for (int k = 0; k + 1 < kSubSteps; ++k) raw[k] = raw[k + 1];
+                raw[kSubSteps - 1] =
+                    load_raw<DT, VEC>(row, min(i + kSubSteps, s1 - 1) * kWave + lane, d.groups, p.V);
+                double wg[GN], sum = 0.0;
+                int mine_last = -1;
 #pragma unroll
-                    for (int j = 0; j < GN; ++j) any |= x[j] > -INFINITY && x[j] >= low;
-                    if (!__ballot(any)) continue;
-                    double wg[GN], sum = 0.0;
-                    int mine_last = -1;
+                for (int j = 0; j < GN; ++j) {
+                    const bool kept = x[j] >= low;
+                    wg[j] = kept ? weight_of(x[j]) : 0.0;
+                    sum += wg[j];
+                    if (wg[j] > 0.0) mine_last = (int)(g * GN + j);
+                }
+                double all;
+                const double inc = wave_inclusive_sum(sum, all);
+                const double prev = wave_shift_up1(inc);
+                const uint64_t hit = __ballot(run + inc > at);
+                if (hit) {
+                    double a = run + (lane ? prev : 0.0);
+                    int tok = -1;
 #pragma unroll
                     for (int j = 0; j < GN; ++j) {
-                        const bool kept = x[j] > -INFINITY && x[j] >= low;
-                        wg[j] = kept ? weight_of(x[j]) : 0.0;
-                        sum += wg[j];
-                        if (wg[j] > 0.0) mine_last = (int)(g * GN + j);
+                        a += wg[j];
+                        if (tok < 0 && a > at && wg[j] > 0.0) tok = (int)(g * GN + j);
                     }
-                    double all;
-                    const double inc = wave_inclusive_sum(sum, all);
-                    const double prev = wave_shift_up1(inc);
-                    const uint64_t hit = __ballot(run + inc > at);
-                    if (hit) {
-                        double a = run + (lane ? prev : 0.0);
-                        int tok = -1;
-#pragma unroll
-                        for (int j = 0; j < GN; ++j) {
-                            a += wg[j];
-                            if (tok < 0 && a > at && wg[j] > 0.0) tok = (int)(g * GN + j);
-                        }
-                        if (tok < 0) tok = mine_last;
-                        token = __builtin_amdgcn_readlane(tok, (int)__builtin_ctzll(hit));
-                    }
-                    run += all;
-                    last = max(last, wave_reduce(mine_last, MaxI32()));
+                    if (tok < 0) tok = mine_last;
+                    token = __builtin_amdgcn_readlane(tok, (int)__builtin_ctzll(hit));
                 }
+                run += all;
+                last = max(last, wave_reduce(mine_last, MaxI32()));
             }
             if (token < 0) token = last;
         }
@@ -878,19 +946,20 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         const double inv = 1.0 / S;
         float* out = p.out_probs + b * p.V;
         const bool vec = p.V % 4 == 0 && (uintptr_t)p.out_probs % 16 == 0;
-        stream_row<DT, VEC>(row, d, p.V, [&](uint32_t, uint32_t g, const float (&x)[GN]) {
+        stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t g, const float (&x)[GN]) {
             float q[GN];
             bool any = false;
 #pragma unroll
             for (int j = 0; j < GN; ++j) {
                 q[j] = 0.0f;
-                any |= x[j] > -INFINITY && x[j] >= low;
+                any |= x[j] >= low;
             }
             if (__ballot(any)) {
 #pragma unroll
                 for (int j = 0; j < GN; ++j)
-                    if (x[j] > -INFINITY && x[j] >= low) q[j] = (float)(weight_of(x[j]) * inv);
+                    if (x[j] >= low) q[j] = (float)(weight_of(x[j]) * inv);
             }
+            if (i >= d.steps) return;  // uniform
             const int64_t i0 = (int64_t)g * GN;
             if (vec && i0 + GN <= p.V) {
 #pragma unroll
@@ -968,8 +1037,6 @@ __device__ __forceinline__ void pick_load(const PickParams& p, int64_t b, int c,
         r[j] = v > 0.0 ? v : 0.0;
     }
 }
-
-struct SumF64 { __device__ double operator()(double a, double b) const { return a + b; } };
 
 __global__ __launch_bounds__(kPickThreads) void pick_chunk_kernel(PickParams p)
 {
