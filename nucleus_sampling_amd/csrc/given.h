@@ -10,20 +10,25 @@
 // are carried to about 1e-13 (doubles and 45-bit integers), not to the 1e-7
 // that the race needs.
 //
-// Weights.  y = (x - x0) s with s = 32 log2(e) / T and x0 the max of the
-// first tokens loaded, the anchor: a cell a = rint(y) spans a thirty-second of
-// an octave of weight, and a token of cell a weighs
+// Weights.  y = x s + b with s = 32 log2(e) / T and b the integer that puts
+// the max of the first tokens loaded, the anchor, near y = 2048: a cell
+// a = rint(y) spans a thirty-second of an octave of weight, and a token of
+// cell a weighs
 //
 //     2^(a/32) * 2^(h/32),   h = y - a in [-1/2, 1/2],
 //
 // the second factor by a polynomial of degree 4 (off by less than 8e-14).
+// Adding 1.5 2^52 in the fused product rounds x s + b to a and leaves it in
+// the low word of the double; h comes from a second fused product, so a cell
+// and its h cost three operations.
+//
 // Cells do not move with the row max, so one pass finds the max and
 // histograms the row.  A histogram slot sums the second factors as integers of
 // `bits` fractional bits (62 - ceil(log2 V), at most 50): exact in any order.
 // The window holds 2048 cells (64 octaves) below the anchor and 2048 above
-// it; what is further down weighs less than 2^-64 of the
-// max each and is counted only.  A row whose max lies above the window takes
-// the pass again.
+// it; what is further down weighs less than 2^-64 of the max each, less than
+// the sums resolve: it is counted, and has no mass.  A row whose max lies above
+// the window takes the pass again.
 //
 // The cuts.  With the cells ranked down from the max's (rank 0), top-k or
 // min-p cut through one bottom cell rb.  The survivors' mass S lies between
@@ -32,7 +37,7 @@
 // pass sums the tokens above r_lo per index segment and lists those of the
 // cells [r_lo, r_hi] and rb; the list then gives rb's exact survivors, S, the
 // crossing cell and by radix select (select.h) the exact cut level.  A row
-// with more than kGivenCap such tokens reads them from memory again wherever
+// with more than kCap such tokens reads them from memory again wherever
 // the list would have been read.
 //
 // One workgroup per row; the draw finds its segment from the segments' sums,
@@ -45,17 +50,15 @@
 
 namespace nucleus {
 
-constexpr int kGivenThreads = 1024;
-constexpr int kGivenWaves = kGivenThreads / kWave;
 constexpr int kOctave = 32;       // cells per octave of weight
 constexpr int kSlots = 4096;      // histogram window
 constexpr int kSlotsBelow = 2048; // of it, below the anchor: 64 octaves
-constexpr int kGivenCap = 8192;   // listed tokens of undecided cells
-constexpr int kSubs = 1024;       // index segments, at most
+constexpr int kCopy = kSlots + kWave + 16;  // words between the two copies
+static_assert(kCopy * 8 % 256 == 128, "copies half the banks apart");
 constexpr int kSubSteps = 4;      // steps of a segment, at least
 constexpr int kRankNone = 0x7FFFFFFF;
-constexpr int kFarDown = -(1 << 17); // a slot whose weight is 0 in double
 constexpr double kLn2 = 0.69314718055994530942;
+constexpr uint32_t kEmpty = 0x7FC00000u;  // (NaN) an empty place of the list
 
 struct GivenParams {
     const void* logits;        // [B, stride]
@@ -85,21 +88,74 @@ __device__ constexpr double kRoot[kOctave] = {
     1.9571441241754002};
 
 // The row's lattice.
+constexpr double kMagic = 0x1.8p52;  // adding it rounds to an integer
 struct Cells {
-    double s;   // cells per logit unit
-    double x0;  // the anchor: its slot is kSlotsBelow
+    double s;    // cells per logit unit
+    double bm;   // b + kMagic
+    float lo;    // fast rows: a logit just below the window
+    bool fast;   // such a logit exists, and lies less than 2^30 cells down
 };
 
-__device__ __forceinline__ Cells uniform(const Cells& c) { return Cells{uniform(c.s), uniform(c.x0)}; }
+// The lattice of a row with anchor x0 (finite) and temperature T > 0.
+__device__ __forceinline__ Cells make_cells(float x0, float T)
+{
+    Cells c;
+    // T = +inf: cells wider than any logit, so that every weight is 1.
+    c.s = T == INFINITY ? 0x1p-1000 : (kOctave * 1.4426950408889634074) / (double)T;
+    // Past |x0| s = 2^44 neighbouring logits are 2^20 cells apart and more,
+    // that is of weight 0 beside each other, whatever s is; b stays an exact
+    // integer.
+    const double ax = fabs((double)x0);
+    if (ax * c.s > 0x1p44) c.s = 0x1p44 / ax;
+    c.s = uniform(c.s);
+    c.bm = uniform(rint((double)kSlotsBelow - (double)x0 * c.s) + kMagic);
+    const double lo = (double)x0 - (double)(kSlotsBelow + 16) / c.s;
+    float f = (float)lo;
+    if ((double)f > lo) f = nextafterf(f, -INFINITY);
+    c.lo = uniform(f);
+    c.fast = c.lo > -INFINITY;
+    return c;
+}
 
 // Slot of a logit (far below the window, and for -inf: negative; above:
-// >= kSlots; saturated to int32) and its place h in its cell.  Monotone in x.
+// >= kSlots; saturated to int32) and its place h in its cell (no number for
+// -inf, and without meaning far outside the window).  Monotone in x.
 __device__ __forceinline__ int slot_of(const Cells& c, float x, double& h)
 {
-    const double y = fma((double)x - c.x0, c.s, (double)kSlotsBelow);
-    const double a = rint(y);
-    h = y - a;
-    return cvt_i32_sat(a);
+    const double t = fma((double)x, c.s, c.bm);
+    h = fma((double)x, c.s, c.bm - t);
+    return cvt_i32_sat(t - kMagic);
+}
+
+// Keeps the instructions before it before it.  The per-token arithmetic below
+// is a chain of dependent double operations, each of which waits about ten
+// cycles for the one before; written one operation for all the tokens of a
+// group at a time, the tokens fill each other's waits (left to itself the
+// compiler finishes one token before it starts the next).
+__device__ __forceinline__ void in_step() { __builtin_amdgcn_sched_barrier(0); }
+
+// The same for N tokens with c.lo <= x of a fast row (FAST: the slot is the
+// low word of the rounded sum; above the window's reach, 2^31 cells, it is
+// without meaning).
+template <int N, bool FAST>
+__device__ __forceinline__ void slots_of(const Cells& c, const float (&x)[N], int (&sl)[N], double (&h)[N])
+{
+    double xd[N], t[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) xd[j] = (double)x[j];
+    in_step();
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = fma(xd[j], c.s, c.bm);
+    in_step();
+#pragma unroll
+    for (int j = 0; j < N; ++j) h[j] = c.bm - t[j];
+    in_step();
+#pragma unroll
+    for (int j = 0; j < N; ++j) h[j] = fma(xd[j], c.s, h[j]);
+    in_step();
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        sl[j] = FAST ? (int)(uint32_t)__double_as_longlong(t[j]) : cvt_i32_sat(t[j] - kMagic);
 }
 
 // 2^(h/32) for |h| <= 1/2: Taylor's polynomial of degree 5 with its last term
@@ -113,6 +169,23 @@ constexpr double kP1 = kL - kL5 * 5 / 256, kP2 = kL * kL / 2, kP3 = kL * kL * kL
 __device__ __forceinline__ double in_cell(double h)
 {
     return fma(fma(fma(fma(kP4, h, kP3), h, kP2), h, kP1), h, 1.0);
+}
+
+template <int N>
+__device__ __forceinline__ void in_cells(const double (&h)[N], double (&q)[N])
+{
+#pragma unroll
+    for (int j = 0; j < N; ++j) q[j] = fma(kP4, h[j], kP3);
+    in_step();
+#pragma unroll
+    for (int j = 0; j < N; ++j) q[j] = fma(q[j], h[j], kP2);
+    in_step();
+#pragma unroll
+    for (int j = 0; j < N; ++j) q[j] = fma(q[j], h[j], kP1);
+    in_step();
+#pragma unroll
+    for (int j = 0; j < N; ++j) q[j] = fma(q[j], h[j], 1.0);
+    in_step();
 }
 
 // The same times 2^bits, rounded to an integer (below 2^52: added to 2^52, it
@@ -129,6 +202,25 @@ struct Fixed {
         return (uint64_t)__double_as_longlong(fma(fma(fma(fma(c4, h, c3), h, c2), h, c1), h, c0)) -
                0x4330000000000000ull;
     }
+    template <int N>
+    __device__ __forceinline__ void operator()(const double (&h)[N], uint64_t (&n)[N]) const
+    {
+        double q[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = fma(c4, h[j], c3);
+        in_step();
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = fma(q[j], h[j], c2);
+        in_step();
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = fma(q[j], h[j], c1);
+        in_step();
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = fma(q[j], h[j], c0);
+        in_step();
+#pragma unroll
+        for (int j = 0; j < N; ++j) n[j] = (uint64_t)__double_as_longlong(q[j]) - 0x4330000000000000ull;
+    }
 };
 
 // The integer nearest to v < 2^52.
@@ -142,6 +234,9 @@ __device__ __forceinline__ double rank_weight(const double* root, int rank)
 {
     return ldexp(root[-rank & (kOctave - 1)], -rank >> 5);
 }
+
+// The lanes for which `v` holds, as a mask in scalar registers.
+__device__ __forceinline__ uint64_t lanes(bool v) { return __builtin_amdgcn_ballot_w64(v); }
 
 // A group: the 16 bytes of a row that a lane loads at a time.
 template <int DT> struct Group { static constexpr int N = DT == kF32 ? 4 : 8; };
@@ -222,30 +317,31 @@ struct Deal {
     uint32_t spw;     // segments per wave
 };
 
-template <int DT>
+template <int DT, int NT>
 __device__ __forceinline__ Deal deal_out(int64_t V)
 {
     Deal d;
     d.groups = (uint32_t)((V + Group<DT>::N - 1) / Group<DT>::N);
-    d.steps = (d.groups + kGivenThreads - 1) / kGivenThreads;
-    d.sps = max((uint32_t)kSubSteps, (d.steps + kSubs / kGivenWaves - 1) / (kSubs / kGivenWaves));
+    d.steps = (d.groups + NT - 1) / NT;
+    d.sps = max((uint32_t)kSubSteps, (d.steps + kWave - 1) / kWave);  // at most 64 segments per wave
     d.spw = (d.steps + d.sps - 1) / d.sps;
     return d;
 }
 
 // fn(step, group, tokens) over the wave's steps, in order, with the loads of
-// the next steps (16 tokens of a lane) in flight.  Every lane takes every step
+// the next steps (128 bytes of a lane) in flight.  Every lane takes every step
 // (past the row's end with tokens of -inf).
 template <int DT, bool VEC, class Fn>
 __device__ __forceinline__ void stream_row(const void* row, const Deal& d, int64_t V, Fn fn)
 {
-    constexpr int GN = Group<DT>::N, AT = VEC ? 16 / GN : 1;
-    const uint32_t lane = threadIdx.x & (kWave - 1), g0 = (threadIdx.x / kWave) * d.steps * kWave + lane;
+    constexpr int GN = Group<DT>::N, AT = VEC ? (DT == kF32 ? 8 : 4) : 2;
+    const uint32_t lane = threadIdx.x & (kWave - 1), g0 = uniform(threadIdx.x / kWave) * d.steps * kWave;
+    const uint32_t whole = (uint32_t)(V / GN);  // groups without the row's end
     u32x4 a[AT], b[AT];
     auto fetch = [&](u32x4 (&to)[AT], uint32_t i) {
 #pragma unroll
         for (int k = 0; k < AT; ++k)
-            to[k] = load_raw<DT, VEC>(row, g0 + min(i + k, d.steps - 1) * kWave, d.groups, V);
+            to[k] = load_raw<DT, VEC>(row, g0 + min(i + k, d.steps - 1) * kWave + lane, d.groups, V);
     };
     fetch(a, 0);
 #pragma unroll 1
@@ -253,32 +349,38 @@ __device__ __forceinline__ void stream_row(const void* row, const Deal& d, int64
         fetch(b, i + AT);
 #pragma unroll
         for (int k = 0; k < AT; ++k) {
+            if (k > 0 && i + k >= d.steps) break;  // uniform
             const uint32_t g = g0 + (i + k) * kWave;
             float x[GN];
-            // Steps past the wave's last read tokens of the next wave: -inf.
-            const bool edge = uniform((int)(i + k >= d.steps || (int64_t)(g - lane + kWave) * GN > V)) != 0;
-            tokens_of<DT>(a[k], g, edge, i + k < d.steps ? V : 0, x);
-            fn(i + k, g, x);
+            tokens_of<DT>(a[k], g + lane, g + kWave > whole, V, x);
+            fn(i + k, g + lane, x);
         }
 #pragma unroll
         for (int k = 0; k < AT; ++k) a[k] = b[k];
     }
 }
 
+template <int NT>
 struct GivenShared {
-    // Integer masses of the cells; from the second pass on, the slots of the
-    // surely kept cells hold their 2^(-rank/32) as doubles instead, and the last
-    // one 0.
-    uint64_t hist[kSlots + 1];
-    uint32_t cnt[kSlots];
-    uint2 list[kGivenCap];     // logit, index
-    double sub[kSubs];         // mass of each segment's surely kept tokens; then of the segments up to it (-1: empty)
-    uint64_t subc[kSubs];      // mass of its kept listed tokens, at 2^-bits
-    double pre[kSubs];         // number of its undecided tokens; then mass of the segments before it
+    static constexpr int kCap = NT < 512 ? NT * 12 : 6144;  // listed tokens of undecided cells
+    static constexpr int kWaves = NT / kWave;
+    // Integer masses of the cells (and a slot per lane for the tokens outside).
+    // Odd lanes add into a second copy, half a row of banks away, which halves
+    // the tokens of one cell that meet at one address (cells that hold
+    // a few percent of the row are common).  In the second pass the second
+    // copy's place holds the weights 2^(-rank/32) of the surely kept cells, as
+    // doubles, and 0 elsewhere.
+    uint64_t hist[2 * kCopy];
+    uint32_t cnt[kSlots + kWave];
+    uint2 list[kCap];          // logit, index
+    double sub[NT];            // mass of each segment's surely kept tokens; then of the segments up to it (-1: empty)
+    uint64_t subc[NT];         // mass of its kept listed tokens, at 2^-bits
+    double pre[NT];            // number of its undecided tokens; then mass of the segments before it
     double root[kOctave];
     SelectShared sel;
-    uint64_t red64[kGivenWaves];
-    double redf[kGivenWaves];
+    uint64_t red64[kWaves];
+    double redf[kWaves];
+    int first[2][kWaves];
     uint32_t list_n;
     // decided by one thread, read by all
     double s_above, a_lo, w_bottom;
@@ -293,6 +395,7 @@ struct MaxF32 { __device__ float operator()(float a, float b) const { return fma
 
 // Exclusive prefix sum over the workgroup's threads in one fixed order;
 // `total` is the whole sum.
+template <int NT>
 __device__ __forceinline__ double block_exclusive_sum_f64(double v, double* scratch, double& total)
 {
     const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
@@ -304,7 +407,7 @@ __device__ __forceinline__ double block_exclusive_sum_f64(double v, double* scra
     __syncthreads();
     double off = 0.0, all = 0.0;
 #pragma unroll
-    for (int i = 0; i < kGivenWaves; ++i) {
+    for (int i = 0; i < NT / kWave; ++i) {
         if (i == w) off = all;
         all += scratch[i];
     }
@@ -322,56 +425,67 @@ enum : int {
 
 // What the first pass finds (each thread its own).
 struct FirstPass {
-    float m;         // max; NaN or +inf if one was seen
-    uint32_t at;     // without a histogram: the step that first held it
-    bool over;       // a token above the window
-    uint32_t tail;   // for top-k rows: finite tokens below the window
+    float m;           // max; NaN or +inf if one was seen
+    uint32_t at;       // without a histogram: the step that first held it
+    uint32_t finite;   // with counts: tokens above -inf in this wave
 };
 
-template <int DT, bool VEC, bool HIST>
+enum : int { kPassMax = 0, kPassHist = 1, kPassCount = 2 };
+
+// Straight-line over a group's tokens: a token outside the window goes to its
+// lane's own slot past it.
+template <int DT, bool VEC, int PASS, bool FAST, class Shared>
 __device__ __forceinline__ FirstPass first_pass(const void* row, const Deal& d, int64_t V, const Cells& c,
-                                                const Fixed& fx, bool use_k, GivenShared& sh)
+                                                const Fixed& fx, Shared& sh)
 {
     constexpr int GN = Group<DT>::N;
-    FirstPass r = {-INFINITY, 0, false, 0};
+    FirstPass r = {-INFINITY, 0, 0};
+    const uint32_t outside = kSlots + (threadIdx.x & (kWave - 1));
+    uint64_t* hist = sh.hist + (threadIdx.x & 1) * kCopy;
     stream_row<DT, VEC>(row, d, V, [&](uint32_t i, uint32_t, const float (&x)[GN]) {
         float most = x[0];  // IEEE maximum: NaN stays
 #pragma unroll
         for (int j = 1; j < GN; ++j) most = __builtin_elementwise_maximum(most, x[j]);
-        if constexpr (!HIST) {
+        if constexpr (PASS == kPassMax) {
             if (!(most <= r.m)) r.at = i;
         }
         r.m = __builtin_elementwise_maximum(r.m, most);
-        if constexpr (HIST) {
+        if constexpr (PASS != kPassMax) {
+            float xc[GN];
+            int sl[GN];
+            double h[GN];
+            uint64_t q[GN];
 #pragma unroll
             for (int j = 0; j < GN; ++j) {
-                double h;
-                const int sl = slot_of(c, x[j], h);
-                const uint64_t q = fx(h);
-                if ((uint32_t)sl < (uint32_t)kSlots) {
-                    atomicAdd((unsigned long long*)&sh.hist[sl], (unsigned long long)q);
-                    if (use_k) atomicAdd(&sh.cnt[sl], 1u);
-                } else if (sl >= kSlots) {
-                    r.over = true;
-                } else if (use_k) {
-                    r.tail += x[j] > -INFINITY;
-                }
+                xc[j] = FAST ? fmaxf(x[j], c.lo) : x[j];
+                if constexpr (PASS == kPassCount) r.finite += (uint32_t)__builtin_popcountll(lanes(x[j] > -INFINITY));
+            }
+            slots_of<GN, FAST>(c, xc, sl, h);
+            fx(h, q);
+#pragma unroll
+            for (int j = 0; j < GN; ++j) {
+                const uint32_t at = min((uint32_t)sl[j], outside);
+                atomicAdd((unsigned long long*)&hist[at], (unsigned long long)q[j]);
+                if constexpr (PASS == kPassCount) atomicAdd(&sh.cnt[at], 1u);
             }
         }
     });
     return r;
 }
 
-template <int DT, bool VEC>
-__global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
+template <int DT, bool VEC, int NT>
+__global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
 {
     constexpr int GN = Group<DT>::N;
-    __shared__ GivenShared sh;
+    typedef GivenShared<NT> Shared;
+    constexpr int kWaves = Shared::kWaves;
+    constexpr uint32_t kCap = Shared::kCap;
+    __shared__ Shared sh;
     const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
     const int64_t b = blockIdx.x;
     const size_t esz = DT == kF32 ? 4 : 2;
     const void* row = (const char*)p.logits + (size_t)b * (size_t)p.stride * esz;
-    const Deal d = deal_out<DT>(p.V);
+    const Deal d = deal_out<DT, NT>(p.V);
     const double scale = ldexp(1.0, p.bits), inv_scale = ldexp(1.0, -p.bits);
     const Fixed fx(scale);
 
@@ -384,17 +498,13 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
     const bool want_hist = !greedy && P > 0.0f && (P < 1.0f || use_k);
 
     if (t < kOctave) sh.root[t] = kRoot[t];
-    static_assert(kSubs == kGivenThreads, "one segment per thread");
     sh.sub[t] = 0.0;
     sh.pre[t] = 0.0;
     sh.subc[t] = 0;
     if (t == 0) sh.list_n = 0;
 
     // ---- pass 1: max, NaN / +inf, histogram -----------------------------
-    Cells c;
-    // T = +inf: cells wider than any logit, so that every weight is 1.
-    c.s = T == INFINITY ? 0x1p-1000 : (kOctave * 1.4426950408889634074) / (double)T;
-    c.x0 = 0.0;
+    Cells c = {};
     FirstPass f;
     float anchor = -INFINITY;
     if (want_hist) {
@@ -404,39 +514,41 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
 #pragma unroll
         for (int j = 0; j < GN; ++j) anchor = fmaxf(anchor, x[j]);
-        for (int i = t; i <= kSlots; i += kGivenThreads) sh.hist[i] = 0;
-        if (use_k)
-            for (int i = t; i < kSlots; i += kGivenThreads) sh.cnt[i] = 0;
-        anchor = uniform(block_reduce<kGivenThreads>(anchor, MaxF32(), (float*)sh.redf));
+        for (int i = t; i < kSlots; i += NT) {
+            sh.hist[i] = sh.hist[kCopy + i] = 0;
+            sh.cnt[i] = 0;
+        }
+        anchor = uniform(block_reduce<NT>(anchor, MaxF32(), (float*)sh.redf));
     }
     float m = -INFINITY;
     bool hist = want_hist && anchor > -INFINITY && anchor < INFINITY;
     // At most three turns: for the max alone where the first tokens were all
-    // masked, with a histogram, and once more where a token lay above its window.
+    // masked, with a histogram, and once more where the max lay above its window.
 #pragma unroll 1
     for (int turn = 0; turn < 3; ++turn) {
-        if (hist) {
-            c.x0 = (double)anchor;
-            c = uniform(c);
-            f = first_pass<DT, VEC, true>(row, d, p.V, c, fx, use_k, sh);
-        } else {
-            f = first_pass<DT, VEC, false>(row, d, p.V, c, fx, use_k, sh);
-        }
-        // One reduction for the max and whether a token lay above the window
-        // (keys order NaN and +inf above every finite logit here, sign aside).
-        const uint32_t key = order_key(f.m != f.m ? INFINITY : f.m);
-        const uint64_t all = block_reduce<kGivenThreads>((uint64_t)key << 1 | (f.over ? 1 : 0),
-                                                         [](uint64_t a, uint64_t e) {
-                                                             return (a > e ? a | (e & 1) : e | (a & 1));
-                                                         }, sh.red64);
-        m = uniform(key_value((uint32_t)(all >> 1)));
-        if (!want_hist || !(m > -INFINITY && m < INFINITY) || (hist && !(all & 1))) break;
+        if (hist) c = make_cells(anchor, T);
+        if (!hist)
+            f = first_pass<DT, VEC, kPassMax, false>(row, d, p.V, c, fx, sh);
+        else if (use_k && c.fast)
+            f = first_pass<DT, VEC, kPassCount, true>(row, d, p.V, c, fx, sh);
+        else if (use_k)
+            f = first_pass<DT, VEC, kPassCount, false>(row, d, p.V, c, fx, sh);
+        else if (c.fast)
+            f = first_pass<DT, VEC, kPassHist, true>(row, d, p.V, c, fx, sh);
+        else
+            f = first_pass<DT, VEC, kPassHist, false>(row, d, p.V, c, fx, sh);
+        m = uniform(block_reduce<NT>(
+            f.m, [](float a, float e) { return __builtin_elementwise_maximum(a, e); }, (float*)sh.redf));
+        if (!want_hist || !(m > -INFINITY && m < INFINITY)) break;
+        double h;
+        if (hist && uniform(slot_of(c, m, h)) < kSlots) break;
         // Anchored at the row's own max, no token lies above the window.
         anchor = m;
         if (hist) {
-            for (int i = t; i <= kSlots; i += kGivenThreads) sh.hist[i] = 0;
-            if (use_k)
-                for (int i = t; i < kSlots; i += kGivenThreads) sh.cnt[i] = 0;
+            for (int i = t; i < kSlots; i += NT) {
+                sh.hist[i] = sh.hist[kCopy + i] = 0;
+                sh.cnt[i] = 0;
+            }
             __syncthreads();
         }
         hist = true;
@@ -463,15 +575,15 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 for (int j = GN - 1; j >= 0; --j)
                     if (x[j] == m) first = g * GN + j;
             }
-            token = (int)block_reduce<kGivenThreads>(first, MinU32(), (uint32_t*)sh.red64);
+            token = (int)block_reduce<NT>(first, MinU32(), (uint32_t*)sh.red64);
         }
         if (t == 0) p.out_count[b] = mode == kGivenGreedy ? 1 : 0;
-        for (int64_t n = t; n < p.N; n += kGivenThreads) {
+        for (int64_t n = t; n < p.N; n += NT) {
             p.out_token[b * p.N + n] = token;
             if (p.out_logprob) p.out_logprob[b * p.N + n] = mode == kGivenGreedy ? 0.0f : __uint_as_float(0x7FC00000u);
         }
         if (p.out_probs)
-            for (int64_t i = t; i < p.V; i += kGivenThreads) p.out_probs[b * p.V + i] = i == token ? 1.0f : 0.0f;
+            for (int64_t i = t; i < p.V; i += NT) p.out_probs[b * p.V + i] = i == token ? 1.0f : 0.0f;
         return;
     }
     // min-p: w_i >= min_p w_max  <=>  x_i >= m + T ln(min_p), rounded up.
@@ -492,55 +604,52 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
 
     // ---- the cells of the cuts -------------------------------------------
     double hm;  // place of the max in its cell
-    if (mode == kGivenLevel) c.x0 = (double)m;
-    c = uniform(c);
+    if (mode == kGivenLevel) c = make_cells(m, T);
     const int top = uniform(slot_of(c, m, hm));  // slot of rank 0
     hm = uniform(hm);
     int rb = kRankNone;                          // bottom cell
     int r_lo = 0, r_hi = -1;
     const bool cut_p = P < 1.0f;
     if (mode == kGivenCells) {
-        constexpr int PER = kSlots / kGivenThreads;
+        // Thread t looks at ranks PER t .. PER t + PER - 1.
+        constexpr int PER = kSlots / NT;
         double wt[PER], run = 0.0;
         uint32_t ct[PER], crun = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int r = PER * t + i, sl = top - r;
-            const uint64_t hv = sl >= 0 ? sh.hist[sl] : 0;
-            wt[i] = hv ? rank_weight(sh.root, r) * ((double)hv * inv_scale) : 0.0;
-            ct[i] = sl >= 0 && use_k ? sh.cnt[sl] : 0u;
+            uint64_t hv = 0;
+            if (sl >= 0) sh.hist[sl] = hv = sh.hist[sl] + sh.hist[kCopy + sl];  // the copies joined
+            wt[i] = ldexp((double)hv * sh.root[-r & (kOctave - 1)], (-r >> 5) - p.bits);
             run += wt[i];
-            crun += ct[i];
         }
         double total;
-        const double before = block_exclusive_sum_f64(run, sh.redf, total);
+        const double before = block_exclusive_sum_f64<NT>(run, sh.redf, total);
         uint32_t cbefore = 0, tails = 0;
         int rk = kRankNone;
         if (use_k) {
-            cbefore = (uint32_t)block_exclusive_sum<kGivenThreads>(crun, sh.red64);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int sl = top - (PER * t + i);
+                ct[i] = sl >= 0 ? sh.cnt[sl] : 0u;
+                crun += ct[i];
+            }
+            cbefore = (uint32_t)block_exclusive_sum<NT>(crun, sh.red64);
             uint32_t cc = cbefore;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 cc += ct[i];
                 if (rk == kRankNone && cc >= (uint32_t)K && ct[i]) rk = PER * t + i;
             }
-            rk = block_reduce<kGivenThreads>(rk, MinI(), (int*)sh.redf);
-            tails = (uint32_t)block_reduce<kGivenThreads>((uint64_t)f.tail, SumU64(), sh.red64);
+            rk = block_reduce<NT>(rk, MinI(), (int*)sh.redf);
+            tails = (uint32_t)block_reduce<NT>((uint64_t)(lane == 0 ? f.finite : 0), SumU64(), sh.red64);
+            if (t == NT - 1) sh.n_window = cbefore + crun;
         }
         double ht;
         // min-p's threshold is at or below the max, and may lie below the window
-        const int64_t st = tmp > -INFINITY ? (int64_t)slot_of(c, tmp, ht) : (int64_t)-1;
-        const int rt = tmp > -INFINITY ? (int)min((int64_t)top - st, (int64_t)top + 1) : kRankNone;
+        const int rt = tmp > -INFINITY ? top - max(slot_of(c, tmp, ht), -1) : kRankNone;
         rb = min(rk, rt);
         if (cut_p && rb > top) rb = kRankNone;  // below the window: the top-p cut is above it
-        if (t == kGivenThreads - 1) {
-            sh.n_window = cbefore + crun;
-            if (rb > top) {
-                sh.n_above = cbefore + crun;
-                sh.s_above = total;
-                sh.w_bottom = 0.0;
-            }
-        }
         if (rb <= top) {
             const int o = rb - PER * t;
             if (o >= 0 && o < PER) {
@@ -550,7 +659,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 for (int i = 0; i < PER; ++i) {
                     if (i < o) {
                         ab += wt[i];
-                        ca += ct[i];
+                        if (use_k) ca += ct[i];
                     }
                     if (i == o) wb = wt[i];
                 }
@@ -558,48 +667,72 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 sh.n_above = ca;
                 sh.w_bottom = wb;
             }
+        } else if (t == NT - 1) {
+            sh.n_above = cbefore + crun;
+            sh.s_above = total;
+            sh.w_bottom = 0.0;
         }
-        __syncthreads();
-        if (rb == kRankNone && use_k && !cut_p && (uint64_t)sh.n_window + tails > (uint64_t)K)
+        if (rb != kRankNone || use_k) __syncthreads();
+        if (rb == kRankNone && use_k && !cut_p && tails > (uint32_t)K && sh.n_window < (uint32_t)K)
             rb = top + 1;  // top-k cuts among the tokens below the window: they are listed as one cell
+        if (rb == kRankNone && !cut_p) {  // neither cuts: all that min-p leaves
+            mode = kGivenLevel;
+            level = tmp;
+        }
         if (cut_p) {
-            const double lo = (double)P * sh.s_above, hi = (double)P * (sh.s_above + sh.w_bottom);
-            int first_lo = kRankNone, first_hi = kRankNone, last = -1;
-            double ab = before;
+            // The first cells whose running mass reaches p S for the least and
+            // the most S may be: in each wave by ballot, then over the waves.
+            const double lo = (double)P * (rb == kRankNone ? total : sh.s_above);
+            const double hi = rb == kRankNone ? lo : (double)P * (sh.s_above + sh.w_bottom);
+            int mine_lo = kRankNone, mine_hi = kRankNone;
+            double ab = before, a_lo = 0.0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int r = PER * t + i;
-                if (wt[i] > 0.0 && r < rb) {
-                    last = r;
-                    if (first_lo == kRankNone && ab + wt[i] >= lo) first_lo = r;
-                    if (first_hi == kRankNone && ab + wt[i] >= hi) first_hi = r;
+                const bool cell = wt[i] > 0.0 && r < rb;
+                if (cell && mine_lo == kRankNone && ab + wt[i] >= lo) {
+                    mine_lo = r;
+                    a_lo = ab;
                 }
+                if (cell && mine_hi == kRankNone && ab + wt[i] >= hi) mine_hi = r;
                 ab += wt[i];
             }
-            // One reduction for the three: ranks fit 13 bits, and a minimum is a
-            // maximum of the complement.
-            const auto pack = [](int v) { return (uint64_t)(v < 8191 ? 8191 - v : 0); };
-            const uint64_t three = block_reduce<kGivenThreads>(
-                pack(first_lo) << 40 | pack(first_hi) << 20 | (uint64_t)(last + 1),
-                [](uint64_t a, uint64_t e) {
-                    const uint64_t k0 = 0xFFFFFull, k1 = k0 << 20, k2 = k0 << 40;
-                    return ((a & k2) > (e & k2) ? a & k2 : e & k2) | ((a & k1) > (e & k1) ? a & k1 : e & k1) |
-                           ((a & k0) > (e & k0) ? a & k0 : e & k0);
-                },
-                sh.red64);
-            first_lo = (three >> 40) ? 8191 - (int)(three >> 40) : kRankNone;
-            first_hi = (three >> 20 & 0xFFFFF) ? 8191 - (int)(three >> 20 & 0xFFFFF) : kRankNone;
-            last = (int)(three & 0xFFFFF) - 1;
-            const int end = rb <= top ? rb : last;  // where rounding leaves none above
-            r_lo = min(first_lo, end);
-            r_hi = min(first_hi, end);
-            const int o = r_lo - PER * t;
-            if (o >= 0 && o < PER) {
-                double a = before;
+            const auto first_of = [&](int v) {
+                const uint64_t any = lanes(v != kRankNone);
+                return any ? __builtin_amdgcn_readlane(v, (int)__builtin_ctzll(any)) : kRankNone;
+            };
+            const int w_lo = first_of(mine_lo), w_hi = first_of(mine_hi);
+            if (lane == 0) {
+                sh.first[0][w] = w_lo;
+                sh.first[1][w] = w_hi;
+            }
+            __syncthreads();
+            r_lo = r_hi = kRankNone;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                r_lo = min(r_lo, sh.first[0][i]);
+                r_hi = min(r_hi, sh.first[1][i]);
+            }
+            if (rb == kRankNone && r_lo == kRankNone) {
+                // Rounding leaves none: the last cell with mass.
+                int last = -1;
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
-                    if (i < o) a += wt[i];
-                sh.a_lo = a;
+                    if (wt[i] > 0.0) last = PER * t + i;
+                r_lo = r_hi = block_reduce<NT>(last, MaxI32(), (int*)sh.redf);
+                const int o = r_lo - PER * t;
+                if (o >= 0 && o < PER) {
+                    double a = before;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        if (i < o) a += wt[i];
+                    sh.a_lo = a;
+                }
+            } else {
+                r_lo = min(r_lo, rb);
+                r_hi = min(r_hi, rb);
+                if (mine_lo == r_lo && r_lo != kRankNone) sh.a_lo = a_lo;
+                if (r_lo == rb && t == 0) sh.a_lo = sh.s_above;
             }
         } else {
             r_lo = rb;  // every cell above the bottom one is kept
@@ -615,108 +748,164 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         const int sl = slot_of(c, x, h);
         return sl >= 0 ? top - sl : top + 1;
     };
-    // The weight of a finite token, however far down.
-    auto weight_of = [&](float x) {
+    // The mass of a finite token: 0 below the window.
+    auto mass_of = [&](float x) {
         double h;
         const int sl = slot_of(c, x, h);
-        return rank_weight(sh.root, top - max(sl, kFarDown)) * in_cell(h);
+        return sl >= 0 ? rank_weight(sh.root, top - sl) * in_cell(h) : 0.0;
     };
-    // A logit below every one that may be kept, and above -inf (a cell and a
-    // half of slack covers the roundings).
+    // Its weight beside that of rank 0, however far down.
+    auto weight_of = [&](float x) {
+        const double y = fma((double)x, c.s, c.bm - kMagic), a = rint(y);
+        return rank_weight(sh.root, -max(cvt_i32_sat(a - (double)top), -(1 << 17))) * in_cell(y - a);
+    };
     const float lowest = -3.402823466e38f;
-    float floor_x = fmaxf(level, lowest);
-    const int s_lo = r_lo > top ? -1 : top - r_lo;  // slots above it are surely kept
+    float floor_x = fmaxf(level, lowest);  // kGivenCells: a logit below every one that may be kept, and above -inf
     if (mode == kGivenCells) {
         const int r_end = rb == kRankNone ? r_hi : max(r_hi, rb);  // the last rank that may be kept
-        if (r_end <= top) floor_x = fmaxf((float)(c.x0 + ((double)(top - r_end - kSlotsBelow) - 1.5) / c.s), lowest);
+        // (a cell and a half of slack covers the roundings)
+        if (r_end <= top)
+            floor_x = fmaxf((float)(((double)(top - r_end) - 1.5 - (c.bm - kMagic)) / c.s), lowest);
         if (floor_x > lowest) floor_x = nextafterf(floor_x, -INFINITY);
     }
     floor_x = uniform(floor_x);
 
     // ---- pass 2: masses of the surely kept, list of the undecided -----------
-    const int s_sure = mode == kGivenLevel ? -1 : s_lo;  // tokens above floor_x in slots above it are kept
-    for (int i = s_sure + 1 + t; i <= top; i += kGivenThreads)
-        sh.hist[i] = (uint64_t)__double_as_longlong(rank_weight(sh.root, top - i));
-    if (t == 0) sh.hist[kSlots] = 0;
+    // Slots above s_sure (kGivenLevel: tokens from floor_x up) are surely kept;
+    // those from s_und to it, and s_bot where it is apart from them, undecided.
+    const int s_sure = mode == kGivenLevel || r_lo > top ? -1 : top - r_lo;
+    const int s_und = r_hi > top ? 0 : top - r_hi, s_bot = top - rb;
+    const bool apart = mode == kGivenCells && rb <= top && rb > r_hi;
+    const bool below = mode == kGivenCells && rb == top + 1;  // the undecided are those below the window
+    double* const cell_mass = (double*)(sh.hist + kCopy);
+    for (int i = t; i <= kSlots; i += NT)
+        cell_mass[i] = i > s_sure && i <= top ? rank_weight(sh.root, top - i) : 0.0;
     __syncthreads();
-    // Tokens above floor_x in other slots from s_und up, or in slot s_bot, are
-    // undecided; those below the window (negative slots, far up as unsigned)
-    // are looked at with them.
-    const uint32_t s_und = mode == kGivenLevel || r_hi > top ? 0u : (uint32_t)(top - r_hi);
-    const int s_bot = mode == kGivenLevel || rb > top ? kSlots : top - rb;
-    uint32_t count = 0;                     // kept tokens, of lane 0 and of each lane
+    uint32_t count = 0;                     // kept tokens, of each lane and of lane 0's wave
     uint32_t kmin = 0xFFFFFFFFu, kmax = 0;  // keys of the undecided that are not listed
     {
-        double acc = 0.0;
+        double acc[2] = {0.0, 0.0};
         uint32_t seg_left = d.sps, seg = (uint32_t)w * d.spw, sure_n = 0, und_n = 0;
-        stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t g, const float (&x)[GN]) {
-            float most = x[0];
-#pragma unroll
-            for (int j = 1; j < GN; ++j) most = fmaxf(most, x[j]);
-            if (__ballot(most >= floor_x)) {  // uniform: most steps of most rows hold no such token
-                uint64_t some[GN];  // lanes whose j-th token is undecided or below the window
-                uint32_t n = 0;
-#pragma unroll
-                for (int j = 0; j < GN; ++j) {
-                    double h;  // (finite: a -inf here would make the sum NaN)
-                    const int sl = slot_of(c, fmaxf(x[j], floor_x), h);
-                    const bool in = x[j] >= floor_x, sure = in && sl > s_sure;
-                    const uint64_t e = sh.hist[sure ? sl : kSlots];
-                    acc = fma(__longlong_as_double((long long)e), in_cell(h), acc);
-                    sure_n += (uint32_t)__builtin_popcountll(__ballot(sure));
-                    some[j] = __ballot(in && !sure && ((uint32_t)sl >= s_und || sl == s_bot));
-                    n += (uint32_t)__builtin_popcountll(some[j]);
-                }
-                if (n) {  // uniform
-                    if (mode == kGivenLevel || r_lo > top) {
-                        // Tokens below the window: kept by their own weight, unless
-                        // top-k cuts among them (they are then one cell).
-#pragma unroll
-                        for (int j = 0; j < GN; ++j)
-                            if (some[j] >> lane & 1) {
-                                if (rb != top + 1) {
-                                    acc += weight_of(x[j]);
-                                    ++count;
-                                }
-                            }
-                    }
-                    if (mode == kGivenCells && r_lo != kRankNone) {
-                        // One LDS atomic reserves the wave's places in the list.
-                        und_n += n;
-                        uint32_t at = 0;
-                        if (lane == 0) at = atomicAdd(&sh.list_n, n);
-                        at = uniform(at);
-#pragma unroll
-                        for (int j = 0; j < GN; ++j) {
-                            if (some[j] >> lane & 1) {
-                                const uint32_t mine = at + __builtin_amdgcn_mbcnt_hi(
-                                    (uint32_t)(some[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some[j], 0));
-                                if (mine < kGivenCap) {
-                                    sh.list[mine] = make_uint2(__float_as_uint(x[j]), g * GN + j);
-                                } else {
-                                    const uint32_t key = order_key(x[j]);
-                                    kmin = min(kmin, key);
-                                    kmax = max(kmax, key);
-                                }
-                            }
-                            at += (uint32_t)__builtin_popcountll(some[j]);
-                        }
-                    }
-                }
+        uint32_t next = 0, left = 0;  // this wave's next place in the list, and how many it has
+        // Lists the tokens whose lanes are in some[j], n in all.
+        auto put = [&](const float (&x)[GN], const uint64_t (&some)[GN], uint32_t n, uint32_t g) {
+            und_n += n;
+            if (n > left) {
+                // The next places of the list, in 64s (one LDS atomic): what is
+                // left of the last ones stays empty.
+                if (lane < left && next + lane < kCap) sh.list[next + lane].x = kEmpty;
+                left = (n + kWave - 1) / kWave * kWave;
+                uint32_t at = 0;
+                if (lane == 0) at = atomicAdd(&sh.list_n, left);
+                next = uniform(at);
             }
+            left -= n;
+#pragma unroll
+            for (int j = 0; j < GN; ++j) {
+                if (some[j] >> lane & 1) {
+                    const uint32_t mine = next + __builtin_amdgcn_mbcnt_hi(
+                        (uint32_t)(some[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some[j], 0));
+                    if (mine < kCap) {
+                        sh.list[mine] = make_uint2(__float_as_uint(x[j]), g * GN + j);
+                    } else {
+                        const uint32_t key = order_key(x[j]);
+                        kmin = min(kmin, key);
+                        kmax = max(kmax, key);
+                    }
+                }
+                next += (uint32_t)__builtin_popcountll(some[j]);
+            }
+        };
+        auto end_step = [&](uint32_t i) {
             if (--seg_left == 0 || i + 1 == d.steps) {
-                const double sum = wave_reduce(acc, SumF64());
+                const double sum = wave_reduce(acc[0] + acc[1], SumF64());
                 if (lane == 0) {
                     sh.sub[seg] = sum;
                     sh.pre[seg] = (double)und_n;
                 }
-                acc = 0.0;
+                acc[0] = acc[1] = 0.0;
                 und_n = 0;
                 ++seg;
                 seg_left = d.sps;
             }
-        });
+        };
+        if (mode == kGivenLevel && c.fast) {
+            stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t, const float (&x)[GN]) {
+                double e[GN], q[GN], h[GN];
+                float xc[GN];
+                int sl[GN];
+#pragma unroll
+                for (int j = 0; j < GN; ++j) {
+                    const bool in = x[j] >= floor_x;
+                    xc[j] = fmaxf(in ? x[j] : c.lo, c.lo);
+                    sure_n += (uint32_t)__builtin_popcountll(lanes(in));
+                }
+                slots_of<GN, true>(c, xc, sl, h);
+#pragma unroll
+                for (int j = 0; j < GN; ++j) e[j] = cell_mass[min((uint32_t)sl[j], (uint32_t)kSlots)];
+                in_cells(h, q);
+#pragma unroll
+                for (int j = 0; j < GN; ++j) acc[j & 1] = fma(e[j], q[j], acc[j & 1]);
+                end_step(i);
+            });
+        } else if (c.fast && !below) {
+            // (a token below floor_x falls into a slot of no mass below s_und)
+            const float from = fmaxf(floor_x, c.lo);
+            stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t g, const float (&x)[GN]) {
+                float most = x[0];
+#pragma unroll
+                for (int j = 1; j < GN; ++j) most = fmaxf(most, x[j]);
+                if (lanes(most >= floor_x)) {  // uniform: most steps of many rows hold no such token
+                    uint64_t some[GN];
+                    uint32_t n = 0;
+                    double e[GN], q[GN], h[GN];
+                    float xc[GN];
+                    int sl[GN];
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) xc[j] = fmaxf(x[j], from);
+                    slots_of<GN, true>(c, xc, sl, h);
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) e[j] = cell_mass[min((uint32_t)sl[j], (uint32_t)kSlots)];
+                    in_cells(h, q);
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) {
+                        // (one comparison to a mask: masks are combined in scalar registers)
+                        const uint64_t up = lanes(sl[j] > s_sure);
+                        sure_n += (uint32_t)__builtin_popcountll(up);
+                        some[j] = lanes(sl[j] >= s_und) & ~up;
+                        if (apart) some[j] |= lanes(sl[j] == s_bot);
+                        n += (uint32_t)__builtin_popcountll(some[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) acc[j & 1] = fma(e[j], q[j], acc[j & 1]);
+                    if (n) put(x, some, n, g);  // uniform
+                }
+                end_step(i);
+            });
+        } else {
+            // Rows whose window reaches past the finite logits, and top-k cuts
+            // below the window.
+            stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t g, const float (&x)[GN]) {
+                uint64_t some[GN];
+                uint32_t n = 0;
+#pragma unroll
+                for (int j = 0; j < GN; ++j) {
+                    double h;  // (finite tokens only: a -inf here would make the sum NaN)
+                    const bool in = x[j] >= floor_x;
+                    const int sl = slot_of(c, fmaxf(x[j], floor_x), h);
+                    const bool sure = mode == kGivenLevel ? in : in & (sl > s_sure);
+                    if (sure & (sl >= 0)) acc[0] = fma(cell_mass[min(sl, kSlots)], in_cell(h), acc[0]);
+                    sure_n += (uint32_t)__builtin_popcountll(lanes(sure));
+                    const bool und = below ? sl < 0 : (sl >= s_und) | (apart & (sl == s_bot));
+                    some[j] = mode == kGivenLevel ? 0 : lanes(in & !sure & und);
+                    n += (uint32_t)__builtin_popcountll(some[j]);
+                }
+                if (n) put(x, some, n, g);  // uniform
+                end_step(i);
+            });
+        }
         if (lane == 0) count += sure_n;
+        if (lane < left && next + lane < kCap) sh.list[next + lane].x = kEmpty;
     }
     __syncthreads();
 
@@ -725,21 +914,21 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
     double one_weight = 0.0;  // every undecided token is kept, with this weight
     if (mode == kGivenCells) {
         const uint32_t ln = sh.list_n;
-        const bool listed = ln <= kGivenCap;
+        const bool listed = ln <= kCap;
         // Every undecided token (key, index), from the list or from memory.
         auto undecided = [&](auto fn) {
             const uint32_t n = listed ? ln : (uint32_t)p.V;
 #pragma unroll 1
-            for (uint32_t i = t; i < n; i += kGivenThreads) {
+            for (uint32_t i = t; i < n; i += NT) {
                 float x;
                 uint32_t idx = i;
                 if (listed) {
-                    x = __uint_as_float(sh.list[i].x);
+                    x = __uint_as_float(sh.list[i].x);  // (kEmpty is NaN)
                     idx = sh.list[i].y;
                 } else {
                     x = logit_at<DT>(row, i);
-                    if (!(x >= floor_x)) continue;
                 }
+                if (!(x >= floor_x)) continue;
                 double h;
                 const int r = rank_of(x, h);
                 if (r >= r_lo && (r <= r_hi || r == rb)) fn(x, idx, r, h);
@@ -748,18 +937,19 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         // Keys that bound those of rank r's cell (a tenth of a cell to spare).
         auto key_at = [&](int r, double off) {
             if (r > top) return off < 0.0 ? 0u : 0xFFFFFFFFu;
-            return order_key((float)(c.x0 + ((double)(top - r - kSlotsBelow) + off) / c.s));
+            return order_key((float)(((double)(top - r) + off - (c.bm - kMagic)) / c.s));
         };
         // Long runs of one value (more undecided tokens than the list holds,
         // all of one key): they share a fate, which needs no search.
         uint32_t one_key = 0;
         if (!listed) {
-            for (uint32_t i = t; i < kGivenCap; i += kGivenThreads) {
-                const uint32_t key = order_key(__uint_as_float(sh.list[i].x));
-                kmin = min(kmin, key);
-                kmax = max(kmax, key);
+            for (uint32_t i = t; i < kCap; i += NT) {
+                const float x = __uint_as_float(sh.list[i].x);
+                if (!(x >= floor_x)) continue;
+                kmin = min(kmin, order_key(x));
+                kmax = max(kmax, order_key(x));
             }
-            const uint64_t both = block_reduce<kGivenThreads>(
+            const uint64_t both = block_reduce<NT>(
                 (uint64_t)kmax << 32 | (uint32_t)~kmin,
                 [](uint64_t a, uint64_t e) {
                     const uint64_t hi = 0xFFFFFFFF00000000ull;
@@ -810,7 +1000,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
             if (thr) {
                 uint32_t found = one_key;
                 if (!one_key) {
-                    const SelectResult r = select_level<kGivenThreads>(
+                    const SelectResult r = select_level<NT>(
                         [&](auto fn) {
                             undecided([&](float x, uint32_t, int rank, double h) {
                                 const uint32_t key = order_key(x);
@@ -831,21 +1021,21 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                         if (rank == rb && order_key(x) >= bottom) sum += fx(h);
                     });
                 }
-                sum = block_reduce<kGivenThreads>(sum, SumU64(), sh.red64);
+                sum = block_reduce<NT>(sum, SumU64(), sh.red64);
                 s_bottom = rank_weight(sh.root, rb) * ((double)sum * inv_scale);
             }
         }
         cut = bottom;
         if (one_key) {
-            one_weight = one_key >= cut ? weight_of(key_value(one_key)) : 0.0;
-            if (one_key >= cut && t == 0) count += ln;
+            one_weight = one_key >= cut ? mass_of(key_value(one_key)) : 0.0;
+            if (one_key >= cut) count += (uint32_t)sh.pre[t];
         } else {
             // The kept among them, added to their segments.
             undecided([&](float x, uint32_t idx, int, double) {
                 if (order_key(x) >= cut) {
                     const uint32_t step = idx / (GN * kWave), own = step / d.steps;
                     atomicAdd((unsigned long long*)&sh.subc[own * d.spw + (step - own * d.steps) / d.sps],
-                              (unsigned long long)fixed_point(weight_of(x) * scale));
+                              (unsigned long long)fixed_point(mass_of(x) * scale));
                     ++count;
                 }
             });
@@ -855,87 +1045,114 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
     const float low = key_value(cut);  // kept: finite and x >= low
 
     // ---- the draws ---------------------------------------------------------
-    count = (uint32_t)block_reduce<kGivenThreads>((uint64_t)count, SumU64(), sh.red64);
-    const uint32_t subs = d.spw * kGivenWaves;
+    count = (uint32_t)block_reduce<NT>((uint64_t)count, SumU64(), sh.red64);
+    const uint32_t subs = d.spw * kWaves;
     const double mine = sh.sub[t] + one_weight * sh.pre[t] + (double)sh.subc[t] * inv_scale;
     double S;
-    const double prefix = block_exclusive_sum_f64(mine, sh.redf, S);
+    const double prefix = block_exclusive_sum_f64<NT>(mine, sh.redf, S);
     sh.sub[t] = mine > 0.0 ? prefix + mine : -1.0;
     sh.pre[t] = prefix;
     __syncthreads();
     if (t == 0) p.out_count[b] = (int32_t)count;
-    // ln of the kept mass measured from the max itself.
-    const double ln_mass = log(S) - hm * (kLn2 / kOctave);
-    for (int64_t n = w; n < p.N; n += kGivenWaves) {
+    for (int64_t n = w; n < p.N; n += kWaves) {
         const double u = p.u_f64 ? ((const double*)p.uniforms)[b * p.N + n] : (double)((const float*)p.uniforms)[b * p.N + n];
         int token = -1;
+        float xt = 0.0f;  // its logit
         if (u == u) {
-            const double at = (u < 0.0 ? 0.0 : (u > 1.0 ? 1.0 : u)) * S;
-            // The first segment whose running sum exceeds `at`; past the end, the last with mass.
-            uint32_t lo = 0;
-            bool found = false;
-            for (uint32_t i = 0; i < subs && !found; i += kWave) {
-                const double v = sh.sub[i + lane];
-                const uint64_t over = __ballot(v > at), any = __ballot(v >= 0.0);
-                if (over) {
-                    lo = i + (uint32_t)__builtin_ctzll(over);
-                    found = true;
-                } else if (any) {
-                    lo = i + 63u - (uint32_t)__builtin_clzll(any);
-                }
-            }
-            double run = sh.pre[lo];
-            const uint32_t own = lo / d.spw, s0 = own * d.steps + (lo - own * d.spw) * d.sps;
-            const uint32_t s1 = min(s0 + d.sps, (own + 1) * d.steps);
-            int last = -1;
-            u32x4 raw[kSubSteps];
-#pragma unroll
-            for (int k = 0; k < kSubSteps; ++k)
-                raw[k] = load_raw<DT, VEC>(row, min(s0 + k, s1 - 1) * kWave + lane, d.groups, p.V);
+            const double at = (u < 0.0 ? 0.0 : u) * S;
+            // The first segment whose running sum exceeds `at`.
+            uint32_t lo = 0xFFFFFFFFu;
 #pragma unroll 1
-            for (uint32_t i = s0; i < s1 && token < 0; ++i) {
-                const uint32_t g = i * kWave + lane;
-                float x[GN];
-                tokens_of<DT>(raw[0], g, true, p.V, x);
+            for (uint32_t i = 0; i < subs && lo == 0xFFFFFFFFu && u < 1.0; i += kWave) {
+                const uint64_t over = lanes(sh.sub[i + lane] > at);
+                if (over) lo = i + (uint32_t)__builtin_ctzll(over);
+            }
+            if (lo != 0xFFFFFFFFu) {
+                double run = sh.pre[lo];
+                const uint32_t own = lo / d.spw, s0 = own * d.steps + (lo - own * d.spw) * d.sps;
+                const uint32_t s1 = min(s0 + d.sps, (own + 1) * d.steps);
+                u32x4 raw[kSubSteps];
 #pragma unroll
-                for (int k = 0; k + 1 < kSubSteps; ++k) raw[k] = raw[k + 1];
-                raw[kSubSteps - 1] =
-                    load_raw<DT, VEC>(row, min(i + kSubSteps, s1 - 1) * kWave + lane, d.groups, p.V);
-                double wg[GN], sum = 0.0;
-                int mine_last = -1;
+                for (int k = 0; k < kSubSteps; ++k)
+                    raw[k] = load_raw<DT, VEC>(row, min(s0 + k, s1 - 1) * kWave + lane, d.groups, p.V);
+                bool open = true;
+#pragma unroll 1
+                for (uint32_t i = s0; i < s1 && open; ++i) {
+                    const uint32_t g = i * kWave + lane;
+                    float x[GN];
+                    tokens_of<DT>(raw[0], g, true, p.V, x);
 #pragma unroll
-                for (int j = 0; j < GN; ++j) {
-                    const bool kept = x[j] >= low;
-                    wg[j] = kept ? weight_of(x[j]) : 0.0;
-                    sum += wg[j];
-                    if (wg[j] > 0.0) mine_last = (int)(g * GN + j);
-                }
-                double all;
-                const double inc = wave_inclusive_sum(sum, all);
-                const double prev = wave_shift_up1(inc);
-                const uint64_t hit = __ballot(run + inc > at);
-                if (hit) {
-                    double a = run + (lane ? prev : 0.0);
-                    int tok = -1;
+                    for (int k = 0; k + 1 < kSubSteps; ++k) raw[k] = raw[k + 1];
+                    raw[kSubSteps - 1] =
+                        load_raw<DT, VEC>(row, min(i + kSubSteps, s1 - 1) * kWave + lane, d.groups, p.V);
+                    double wg[GN], sum = 0.0;
+                    int mine_at = -1;  // this lane's last token with mass
+                    float x_at = 0.0f;
 #pragma unroll
                     for (int j = 0; j < GN; ++j) {
-                        a += wg[j];
-                        if (tok < 0 && a > at && wg[j] > 0.0) tok = (int)(g * GN + j);
+                        wg[j] = x[j] >= low ? mass_of(x[j]) : 0.0;
+                        sum += wg[j];
+                        if (wg[j] > 0.0) {
+                            mine_at = (int)(g * GN + j);
+                            x_at = x[j];
+                        }
                     }
-                    if (tok < 0) tok = mine_last;
-                    token = __builtin_amdgcn_readlane(tok, (int)__builtin_ctzll(hit));
+                    double all;
+                    const double inc = wave_inclusive_sum(sum, all);
+                    const double prev = wave_shift_up1(inc);
+                    const uint64_t hit = lanes(run + inc > at && mine_at >= 0), any = lanes(mine_at >= 0);
+                    if (hit) {
+                        // The first of the lane's tokens past `at`.
+                        double a = run + (lane ? prev : 0.0);
+                        bool here = true;
+#pragma unroll
+                        for (int j = 0; j < GN; ++j) {
+                            a += wg[j];
+                            if (here && a > at && wg[j] > 0.0) {
+                                mine_at = (int)(g * GN + j);
+                                x_at = x[j];
+                                here = false;
+                            }
+                        }
+                    }
+                    if (any) {  // the lane that holds it, or so far the last with mass
+                        const int L = hit ? (int)__builtin_ctzll(hit) : 63 - (int)__builtin_clzll(any);
+                        token = __builtin_amdgcn_readlane(mine_at, L);
+                        xt = lane_value(x_at, L);
+                    }
+                    open = !hit;
+                    run += all;
                 }
-                run += all;
-                last = max(last, wave_reduce(mine_last, MaxI32()));
+            } else {
+                // At or past the end: the row's last kept token of positive weight.
+#pragma unroll 1
+                for (int64_t i = (int64_t)kWaves * d.steps - 1; i >= 0 && token < 0; --i) {
+                    const uint32_t g = (uint32_t)i * kWave + lane;
+                    float x[GN], x_at = 0.0f;
+                    tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
+                    int mine_at = -1;
+#pragma unroll
+                    for (int j = 0; j < GN; ++j)
+                        if (x[j] >= low && weight_of(x[j]) > 0.0) {
+                            mine_at = (int)(g * GN + j);
+                            x_at = x[j];
+                        }
+                    const uint64_t any = lanes(mine_at >= 0);
+                    if (any) {
+                        const int L = 63 - (int)__builtin_clzll(any);
+                        token = __builtin_amdgcn_readlane(mine_at, L);
+                        xt = lane_value(x_at, L);
+                    }
+                }
             }
-            if (token < 0) token = last;
         }
         if (lane == 0) {
             p.out_token[b * p.N + n] = token;
             if (p.out_logprob) {
                 float lp = __uint_as_float(0x7FC00000u);
                 if (token >= 0)
-                    lp = (float)(((double)logit_at<DT>(row, token) - (double)m) / (double)T - ln_mass);
+                    // (the mass is measured from the max's cell, not from the max itself)
+                    lp = (float)(((double)xt - (double)m) / (double)T - (log(S) - hm * (kLn2 / kOctave)));
                 p.out_logprob[b * p.N + n] = lp;
             }
         }
@@ -946,7 +1163,7 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
         const double inv = 1.0 / S;
         float* out = p.out_probs + b * p.V;
         const bool vec = p.V % 4 == 0 && (uintptr_t)p.out_probs % 16 == 0;
-        stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t g, const float (&x)[GN]) {
+        stream_row<DT, VEC>(row, d, p.V, [&](uint32_t, uint32_t g, const float (&x)[GN]) {
             float q[GN];
             bool any = false;
 #pragma unroll
@@ -954,12 +1171,11 @@ __global__ __launch_bounds__(kGivenThreads) void given_row_kernel(GivenParams p)
                 q[j] = 0.0f;
                 any |= x[j] >= low;
             }
-            if (__ballot(any)) {
+            if (lanes(any)) {
 #pragma unroll
                 for (int j = 0; j < GN; ++j)
                     if (x[j] >= low) q[j] = (float)(weight_of(x[j]) * inv);
             }
-            if (i >= d.steps) return;  // uniform
             const int64_t i0 = (int64_t)g * GN;
             if (vec && i0 + GN <= p.V) {
 #pragma unroll

@@ -19,6 +19,17 @@ bool other_options(const nucleus_options* o)
            o->split_give_up_row;
 }
 
+template <int DT>
+int launch_sample(const GivenParams& p, bool vec, hipStream_t s)
+{
+    const dim3 grid((unsigned)p.B), block(512);
+    if (vec)
+        hipLaunchKernelGGL((given_row_kernel<DT, true, 512>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((given_row_kernel<DT, false, 512>), grid, block, 0, s, p);
+    return hipGetLastError() == hipSuccess ? NUCLEUS_OK : NUCLEUS_ELAUNCH;
+}
+
 size_t uniform_bytes(int32_t dtype) { return dtype == NUCLEUS_F64 ? 8 : 4; }
 
 }  // namespace
@@ -68,20 +79,9 @@ extern "C" int nucleus_sample_given(const void* logits, int64_t B, int64_t V, co
     while ((int64_t(1) << log2v) < V) ++log2v;
     p.bits = 62 - log2v < 50 ? 62 - log2v : 50;
     hipStream_t s = (hipStream_t)o.stream;
-    const dim3 grid((unsigned)B), block(kGivenThreads);
-    if (o.dtype == NUCLEUS_F32 && vec)
-        hipLaunchKernelGGL((given_row_kernel<kF32, true>), grid, block, 0, s, p);
-    else if (o.dtype == NUCLEUS_F32)
-        hipLaunchKernelGGL((given_row_kernel<kF32, false>), grid, block, 0, s, p);
-    else if (o.dtype == NUCLEUS_BF16 && vec)
-        hipLaunchKernelGGL((given_row_kernel<kBF16, true>), grid, block, 0, s, p);
-    else if (o.dtype == NUCLEUS_BF16)
-        hipLaunchKernelGGL((given_row_kernel<kBF16, false>), grid, block, 0, s, p);
-    else if (vec)
-        hipLaunchKernelGGL((given_row_kernel<kF16, true>), grid, block, 0, s, p);
-    else
-        hipLaunchKernelGGL((given_row_kernel<kF16, false>), grid, block, 0, s, p);
-    return hipGetLastError() == hipSuccess ? NUCLEUS_OK : NUCLEUS_ELAUNCH;
+    if (o.dtype == NUCLEUS_F32) return launch_sample<kF32>(p, vec, s);
+    if (o.dtype == NUCLEUS_BF16) return launch_sample<kBF16>(p, vec, s);
+    return launch_sample<kF16>(p, vec, s);
 }
 
 extern "C" size_t nucleus_spec_given_workspace_bytes(int64_t B, int64_t V)
