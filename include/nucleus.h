@@ -368,19 +368,30 @@ int nucleus_project(const void* hidden, const void* weight, int64_t M, int64_t N
  *                   probability in the kept, renormalised distribution,
  *                   (x - m)/T - ln S_keep; 0 for greedy rows, NaN where the token is -1.
  * out_probs         device [B, V] float, or NULL, as for nucleus_sample.
- * opt               NULL, or options with dtype, stream and row_stride used;
- *                   flags, seeds, out_min_kept_logit, out_logprobs, the
- *                   pre-chain and split_give_up_row must be unset
- *                   (NUCLEUS_EINVAL otherwise).
+ * opt               NULL, or options with dtype, stream, row_stride and the
+ *                   workspace used; flags, seeds, out_min_kept_logit,
+ *                   out_logprobs, the pre-chain and split_give_up_row must be
+ *                   unset (NUCLEUS_EINVAL otherwise).  The workspace is
+ *                   optional: with one (at least
+ *                   nucleus_given_workspace_bytes(B, V, dtype) bytes, 256-byte
+ *                   aligned, NUCLEUS_EWORKSPACE otherwise; no initial value
+ *                   needed) long rows of small and middle-sized batches are
+ *                   split over the device; without one (NULL) every row runs
+ *                   on one workgroup, with the same results up to that 1e-13.
  *
  * Returns NUCLEUS_OK or a negative code; asynchronous on opt->stream, and
- * may be captured into a graph.  Results do not depend on the rest of the
- * batch and equal calls give equal bits.  No workspace.
+ * may be captured into a graph; calls that may overlap need different
+ * workspaces.  A row's result does not depend on the other rows' values, and
+ * equal calls give equal bits.
  */
 int nucleus_sample_given(const void* logits, int64_t B, int64_t V, const float* temperature, const float* top_p,
                          const int32_t* top_k, const float* min_p, const void* uniforms, int32_t uniform_dtype,
                          int64_t N, int32_t* out_token, int32_t* out_keep_count, float* out_token_logprob,
                          float* out_probs, const nucleus_options* opt);
+
+/* Device workspace, in bytes, with which nucleus_sample_given splits the rows
+ * of a batch of this shape; 0 where it does not, and for invalid shapes. */
+size_t nucleus_given_workspace_bytes(int64_t B, int64_t V, int32_t dtype);
 
 /*
  * nucleus_spec_verify from random numbers the caller brings (since version

@@ -101,6 +101,8 @@ def lib():
         L.nucleus_sample_given.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, ctypes.c_int32, i64, vp, vp, vp, vp,
                                            ctypes.POINTER(_Options)]
         L.nucleus_sample_given.restype = ctypes.c_int
+        L.nucleus_given_workspace_bytes.argtypes = [i64, i64, ctypes.c_int32]
+        L.nucleus_given_workspace_bytes.restype = ctypes.c_size_t
         L.nucleus_spec_verify_given.argtypes = [vp, vp, vp, i64, i64, vp, ctypes.c_int32, vp, vp, ctypes.POINTER(_Options)]
         L.nucleus_spec_verify_given.restype = ctypes.c_int
         L.nucleus_spec_given_workspace_bytes.argtypes = [i64, i64]
@@ -546,7 +548,7 @@ def _output(t, shape, dtype, name, dev):
 
 def sample_given(logits: torch.Tensor, temperature, top_p, uniforms, top_k=None, min_p=None, *,
                  want_probs: bool = False, out: Optional[GivenResult] = None,
-                 stream: Optional[torch.cuda.Stream] = None) -> GivenResult:
+                 stream: Optional[torch.cuda.Stream] = None, single_workgroup: bool = False) -> GivenResult:
     """The chain of ``sample`` drawn by inverse CDF from ``uniforms`` that the
     caller brings (``nucleus_sample_given``): row b's kept set is that of
     ``sample``, and draw n takes the lowest kept token whose running weight
@@ -557,16 +559,19 @@ def sample_given(logits: torch.Tensor, temperature, top_p, uniforms, top_k=None,
     or float64, in [0, 1).  ``temperature``, ``top_p``, ``top_k`` and
     ``min_p`` are per row, as for ``sample``.  ``want_probs`` also returns
     the kept distribution.  Launches on ``stream`` (default: the current
-    stream) and returns without synchronising."""
+    stream) and returns without synchronising.  ``single_workgroup`` runs
+    every row on one workgroup, without the workspace that long rows of
+    smaller batches are split with; it exists for verification."""
     if not torch.is_tensor(logits) or logits.dtype not in _CODES:
         raise TypeError("logits must be a float32, bfloat16 or float16 tensor")
     if logits.requires_grad and torch.is_grad_enabled():
         raise _inference_only("sample_given")
     dev = _on_gpu(logits, "logits")
-    return _on(dev, stream, _sample_given, dev, logits, temperature, top_p, uniforms, top_k, min_p, want_probs, out)
+    return _on(dev, stream, _sample_given, dev, logits, temperature, top_p, uniforms, top_k, min_p, want_probs, out,
+               single_workgroup)
 
 
-def _sample_given(handle, dev, logits, temperature, top_p, uniforms, top_k, min_p, want_probs, out):
+def _sample_given(handle, dev, logits, temperature, top_p, uniforms, top_k, min_p, want_probs, out, single_workgroup):
     logits, B, V, stride = _matrix(logits, "logits", dev)
     U, ucode = _uniforms(uniforms, dev)
     shape = U.shape
@@ -583,8 +588,13 @@ def _sample_given(handle, dev, logits, temperature, top_p, uniforms, top_k, min_
                       _output(o.logprob, shape, torch.float32, "logprob", dev),
                       _output(o.probs, (B, V), torch.float32, "probs", dev)
                       if want_probs or o.probs is not None else None)
-    opt = _Options(_CODES[logits.dtype], 0, handle, stride)
-    _check((_lib or lib()).nucleus_sample_given(
+    L, code = _lib or lib(), _CODES[logits.dtype]
+    # A workspace of the call's own: its memory is reused in stream order, and
+    # under graph capture it is the graph's.
+    need = 0 if single_workgroup else L.nucleus_given_workspace_bytes(B, V, code)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    opt = _Options(code, 0, handle, stride, ws.data_ptr() if need else None, need)
+    _check(L.nucleus_sample_given(
         logits.data_ptr(), B, V, tp, pp, kp, mp, U.data_ptr(), ucode, N, res.token.data_ptr(),
         res.keep_count.data_ptr(), res.logprob.data_ptr(), None if res.probs is None else res.probs.data_ptr(),
         ctypes.byref(opt)), "nucleus_sample_given")
@@ -618,8 +628,6 @@ def _spec_verify_given(handle, dev, target_probs, draft_probs, draft_token, unif
     o = out if out is not None else SpecResult(None, None)
     res = SpecResult(_output(o.token, (B,), torch.int32, "token", dev),
                      _output(o.accepted, (B,), torch.int32, "accepted", dev))
-    # A workspace of the call's own: its memory is reused in stream order, and
-    # under graph capture it is the graph's.
     L = _lib or lib()
     need = L.nucleus_spec_given_workspace_bytes(B, V)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)

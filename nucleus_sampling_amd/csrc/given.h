@@ -40,9 +40,12 @@
 // with more than kCap such tokens reads them from memory again wherever
 // the list would have been read.
 //
-// One workgroup per row; the draw finds its segment from the segments' sums,
-// then reads that segment alone.
+// The draw finds its segment from the segments' sums, then reads that segment
+// alone.  Short rows and large batches run on one workgroup per row; long rows
+// of smaller batches are split over workgroups (below).
 #pragma once
+
+#include <type_traits>
 
 #include "common.h"
 #include "params.h"
@@ -421,6 +424,7 @@ enum : int {
     kGivenGreedy = 1,
     kGivenLevel = 2,   // kept: x >= a level known at once
     kGivenCells = 3,   // kept: by cells and the listed tokens
+    kGivenAlone = 4,   // (split rows) left to one workgroup
 };
 
 // What the first pass finds (each thread its own).
@@ -473,119 +477,69 @@ __device__ __forceinline__ FirstPass first_pass(const void* row, const Deal& d, 
     return r;
 }
 
-template <int DT, bool VEC, int NT>
-__global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
+// One row's parameters.
+struct RowIn {
+    float T, P, MP;
+    int K;
+    bool greedy, use_k, want_hist;
+};
+
+__device__ __forceinline__ RowIn row_in(const GivenParams& p, int64_t b)
 {
-    constexpr int GN = Group<DT>::N;
-    typedef GivenShared<NT> Shared;
-    constexpr int kWaves = Shared::kWaves;
-    constexpr uint32_t kCap = Shared::kCap;
-    __shared__ Shared sh;
-    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
-    const int64_t b = blockIdx.x;
-    const size_t esz = DT == kF32 ? 4 : 2;
-    const void* row = (const char*)p.logits + (size_t)b * (size_t)p.stride * esz;
-    const Deal d = deal_out<DT, NT>(p.V);
-    const double scale = ldexp(1.0, p.bits), inv_scale = ldexp(1.0, -p.bits);
-    const Fixed fx(scale);
-
-    const float T = uniform(p.temperature[b]), P = uniform(p.top_p[b]);
-    const int K = p.top_k ? uniform(p.top_k[b]) : 0;
-    const float MP = p.min_p ? uniform(p.min_p[b]) : 0.0f;
-    const bool greedy = T <= 0.0f;
-    const bool use_k = K > 0 && (int64_t)K < p.V;
+    RowIn r;
+    r.T = uniform(p.temperature[b]);
+    r.P = uniform(p.top_p[b]);
+    r.K = p.top_k ? uniform(p.top_k[b]) : 0;
+    r.MP = p.min_p ? uniform(p.min_p[b]) : 0.0f;
+    r.greedy = r.T <= 0.0f;
+    r.use_k = r.K > 0 && (int64_t)r.K < p.V;
     // A histogram is needed where a cut has to be searched for.
-    const bool want_hist = !greedy && P > 0.0f && (P < 1.0f || use_k);
+    r.want_hist = !r.greedy && r.P > 0.0f && (r.P < 1.0f || r.use_k);
+    return r;
+}
 
-    if (t < kOctave) sh.root[t] = kRoot[t];
-    sh.sub[t] = 0.0;
-    sh.pre[t] = 0.0;
-    sh.subc[t] = 0;
-    if (t == 0) sh.list_n = 0;
+__device__ __forceinline__ bool row_error(const RowIn& r, float m)
+{
+    return !(m > -INFINITY && m < INFINITY) || isnan(r.T) || isnan(r.P) || isnan(r.MP);
+}
 
-    // ---- pass 1: max, NaN / +inf, histogram -----------------------------
-    Cells c = {};
-    FirstPass f;
-    float anchor = -INFINITY;
-    if (want_hist) {
-        // The anchor: the max of every thread's first group.
-        float x[GN];
-        const uint32_t g = (uint32_t)w * d.steps * kWave + lane;
-        tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
-#pragma unroll
-        for (int j = 0; j < GN; ++j) anchor = fmaxf(anchor, x[j]);
-        for (int i = t; i < kSlots; i += NT) {
-            sh.hist[i] = sh.hist[kCopy + i] = 0;
-            sh.cnt[i] = 0;
-        }
-        anchor = uniform(block_reduce<NT>(anchor, MaxF32(), (float*)sh.redf));
-    }
-    float m = -INFINITY;
-    bool hist = want_hist && anchor > -INFINITY && anchor < INFINITY;
-    // At most three turns: for the max alone where the first tokens were all
-    // masked, with a histogram, and once more where the max lay above its window.
-#pragma unroll 1
-    for (int turn = 0; turn < 3; ++turn) {
-        if (hist) c = make_cells(anchor, T);
-        if (!hist)
-            f = first_pass<DT, VEC, kPassMax, false>(row, d, p.V, c, fx, sh);
-        else if (use_k && c.fast)
-            f = first_pass<DT, VEC, kPassCount, true>(row, d, p.V, c, fx, sh);
-        else if (use_k)
-            f = first_pass<DT, VEC, kPassCount, false>(row, d, p.V, c, fx, sh);
-        else if (c.fast)
-            f = first_pass<DT, VEC, kPassHist, true>(row, d, p.V, c, fx, sh);
-        else
-            f = first_pass<DT, VEC, kPassHist, false>(row, d, p.V, c, fx, sh);
-        m = uniform(block_reduce<NT>(
-            f.m, [](float a, float e) { return __builtin_elementwise_maximum(a, e); }, (float*)sh.redf));
-        if (!want_hist || !(m > -INFINITY && m < INFINITY)) break;
-        double h;
-        if (hist && uniform(slot_of(c, m, h)) < kSlots) break;
-        // Anchored at the row's own max, no token lies above the window.
-        anchor = m;
-        if (hist) {
-            for (int i = t; i < kSlots; i += NT) {
-                sh.hist[i] = sh.hist[kCopy + i] = 0;
-                sh.cnt[i] = 0;
-            }
-            __syncthreads();
-        }
-        hist = true;
-    }
+template <int DT>
+__device__ __forceinline__ const void* row_of(const GivenParams& p, int64_t b)
+{
+    return (const char*)p.logits + (size_t)b * (size_t)p.stride * (DT == kF32 ? 4 : 2);
+}
 
+// How a row's tokens are kept, up to the undecided ones.  Ranks count cells
+// down from the max's; kRankNone stands for none.
+struct RowPlan {
+    Cells c;
+    double hm;        // place of the max in its cell
+    float m;          // max
+    float tmp;        // min-p's threshold (-inf: off)
+    float level;      // kGivenLevel: kept iff x >= level and finite
+    float floor_x;    // finite; every token that may be kept is at or above it
+    int mode;
+    int top;          // slot of rank 0
+    int rb;           // bottom cell; top + 1: the tokens below the window
+    int r_lo, r_hi;   // kept: ranks below r_lo; undecided: r_lo .. r_hi and rb
+};
+
+constexpr float kLowest = -3.402823466e38f;
+
+// From the max (of a row without error, T > 0) and, where the row wants one,
+// the histogram in LDS (`copies`: in two copies) over lattice c; `finite`:
+// tokens above -inf (top-k rows).  s_above, a_lo, w_bottom and n_above are left
+// in LDS.
+template <int NT, class Shared>
+__device__ __forceinline__ RowPlan plan_row(Shared& sh, const RowIn& in, Cells c, float m, uint32_t finite, bool copies,
+                                            int bits)
+{
+    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+    const float T = in.T, P = in.P, MP = in.MP;
+    const int K = in.K;
+    const bool use_k = in.use_k, cut_p = P < 1.0f;
     int mode = kGivenCells;
-    float level = -INFINITY;  // kGivenLevel: kept iff x >= level (and finite)
-    if (!(m > -INFINITY && m < INFINITY) || isnan(T) || isnan(P) || isnan(MP)) {
-        mode = kGivenError;
-    } else if (greedy) {
-        mode = kGivenGreedy;
-    }
-    if (mode == kGivenError || mode == kGivenGreedy) {
-        int token = -1;
-        if (mode == kGivenGreedy) {
-            // The lowest index that holds the max: every thread knows the step
-            // that first held its own.
-            uint32_t first = 0xFFFFFFFFu;
-            if (f.m == m) {
-                const uint32_t g = ((uint32_t)w * d.steps + f.at) * kWave + lane;
-                float x[GN];
-                tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
-#pragma unroll
-                for (int j = GN - 1; j >= 0; --j)
-                    if (x[j] == m) first = g * GN + j;
-            }
-            token = (int)block_reduce<NT>(first, MinU32(), (uint32_t*)sh.red64);
-        }
-        if (t == 0) p.out_count[b] = mode == kGivenGreedy ? 1 : 0;
-        for (int64_t n = t; n < p.N; n += NT) {
-            p.out_token[b * p.N + n] = token;
-            if (p.out_logprob) p.out_logprob[b * p.N + n] = mode == kGivenGreedy ? 0.0f : __uint_as_float(0x7FC00000u);
-        }
-        if (p.out_probs)
-            for (int64_t i = t; i < p.V; i += NT) p.out_probs[b * p.V + i] = i == token ? 1.0f : 0.0f;
-        return;
-    }
+    float level = -INFINITY;
     // min-p: w_i >= min_p w_max  <=>  x_i >= m + T ln(min_p), rounded up.
     float tmp = -INFINITY;
     if (MP > 0.0f && T != INFINITY) {
@@ -597,19 +551,16 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
     if (P <= 0.0f) {
         mode = kGivenLevel;
         level = m;
-    } else if (!want_hist) {
+    } else if (!in.want_hist) {
         mode = kGivenLevel;
         level = tmp;
     }
 
-    // ---- the cells of the cuts -------------------------------------------
-    double hm;  // place of the max in its cell
+    double hm;
     if (mode == kGivenLevel) c = make_cells(m, T);
-    const int top = uniform(slot_of(c, m, hm));  // slot of rank 0
-    hm = uniform(hm);
-    int rb = kRankNone;                          // bottom cell
+    const int top = uniform(slot_of(c, m, hm));
+    int rb = kRankNone;
     int r_lo = 0, r_hi = -1;
-    const bool cut_p = P < 1.0f;
     if (mode == kGivenCells) {
         // Thread t looks at ranks PER t .. PER t + PER - 1.
         constexpr int PER = kSlots / NT;
@@ -619,13 +570,13 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
         for (int i = 0; i < PER; ++i) {
             const int r = PER * t + i, sl = top - r;
             uint64_t hv = 0;
-            if (sl >= 0) sh.hist[sl] = hv = sh.hist[sl] + sh.hist[kCopy + sl];  // the copies joined
-            wt[i] = ldexp((double)hv * sh.root[-r & (kOctave - 1)], (-r >> 5) - p.bits);
+            if (sl >= 0) sh.hist[sl] = hv = sh.hist[sl] + (copies ? sh.hist[kCopy + sl] : 0);  // joined
+            wt[i] = ldexp((double)hv * sh.root[-r & (kOctave - 1)], (-r >> 5) - bits);
             run += wt[i];
         }
         double total;
         const double before = block_exclusive_sum_f64<NT>(run, sh.redf, total);
-        uint32_t cbefore = 0, tails = 0;
+        uint32_t cbefore = 0;
         int rk = kRankNone;
         if (use_k) {
 #pragma unroll
@@ -642,7 +593,6 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
                 if (rk == kRankNone && cc >= (uint32_t)K && ct[i]) rk = PER * t + i;
             }
             rk = block_reduce<NT>(rk, MinI(), (int*)sh.redf);
-            tails = (uint32_t)block_reduce<NT>((uint64_t)(lane == 0 ? f.finite : 0), SumU64(), sh.red64);
             if (t == NT - 1) sh.n_window = cbefore + crun;
         }
         double ht;
@@ -673,7 +623,7 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
             sh.w_bottom = 0.0;
         }
         if (rb != kRankNone || use_k) __syncthreads();
-        if (rb == kRankNone && use_k && !cut_p && tails > (uint32_t)K && sh.n_window < (uint32_t)K)
+        if (rb == kRankNone && use_k && !cut_p && finite > (uint32_t)K && sh.n_window < (uint32_t)K)
             rb = top + 1;  // top-k cuts among the tokens below the window: they are listed as one cell
         if (rb == kRankNone && !cut_p) {  // neither cuts: all that min-p leaves
             mode = kGivenLevel;
@@ -709,7 +659,7 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
             __syncthreads();
             r_lo = r_hi = kRankNone;
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i) {
+            for (int i = 0; i < NT / kWave; ++i) {
                 r_lo = min(r_lo, sh.first[0][i]);
                 r_hi = min(r_hi, sh.first[1][i]);
             }
@@ -743,43 +693,441 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
         rb = uniform(rb);
     }
 
-    // Rank of a finite token's cell; all cells below the window are one.
-    auto rank_of = [&](float x, double& h) {
-        const int sl = slot_of(c, x, h);
-        return sl >= 0 ? top - sl : top + 1;
-    };
-    // The mass of a finite token: 0 below the window.
-    auto mass_of = [&](float x) {
-        double h;
-        const int sl = slot_of(c, x, h);
-        return sl >= 0 ? rank_weight(sh.root, top - sl) * in_cell(h) : 0.0;
-    };
-    // Its weight beside that of rank 0, however far down.
-    auto weight_of = [&](float x) {
-        const double y = fma((double)x, c.s, c.bm - kMagic), a = rint(y);
-        return rank_weight(sh.root, -max(cvt_i32_sat(a - (double)top), -(1 << 17))) * in_cell(y - a);
-    };
-    const float lowest = -3.402823466e38f;
-    float floor_x = fmaxf(level, lowest);  // kGivenCells: a logit below every one that may be kept, and above -inf
+    float floor_x = fmaxf(level, kLowest);
     if (mode == kGivenCells) {
         const int r_end = rb == kRankNone ? r_hi : max(r_hi, rb);  // the last rank that may be kept
         // (a cell and a half of slack covers the roundings)
         if (r_end <= top)
-            floor_x = fmaxf((float)(((double)(top - r_end) - 1.5 - (c.bm - kMagic)) / c.s), lowest);
-        if (floor_x > lowest) floor_x = nextafterf(floor_x, -INFINITY);
+            floor_x = fmaxf((float)(((double)(top - r_end) - 1.5 - (c.bm - kMagic)) / c.s), kLowest);
+        if (floor_x > kLowest) floor_x = nextafterf(floor_x, -INFINITY);
     }
-    floor_x = uniform(floor_x);
+    RowPlan o;
+    o.c = c;
+    o.hm = uniform(hm);
+    o.m = m;
+    o.tmp = tmp;
+    o.level = level;
+    o.floor_x = uniform(floor_x);
+    o.mode = mode;
+    o.top = top;
+    o.rb = rb;
+    o.r_lo = r_lo;
+    o.r_hi = r_hi;
+    return o;
+}
+
+// Rank of a finite token's cell; all cells below the window are one.
+__device__ __forceinline__ int rank_of(const RowPlan& o, float x, double& h)
+{
+    const int sl = slot_of(o.c, x, h);
+    return sl >= 0 ? o.top - sl : o.top + 1;
+}
+
+// The mass of a finite token: 0 below the window.
+__device__ __forceinline__ double mass_of(const RowPlan& o, const double* root, float x)
+{
+    double h;
+    const int sl = slot_of(o.c, x, h);
+    return sl >= 0 ? rank_weight(root, o.top - sl) * in_cell(h) : 0.0;
+}
+
+// Its weight beside that of rank 0, however far down.
+__device__ __forceinline__ double weight_of(const RowPlan& o, const double* root, float x)
+{
+    const double y = fma((double)x, o.c.s, o.c.bm - kMagic), a = rint(y);
+    return rank_weight(root, -max(cvt_i32_sat(a - (double)o.top), -(1 << 17))) * in_cell(y - a);
+}
+
+// A greedy row, or (token -1) one in error.  Every thread of the workgroup.
+template <int NT>
+__device__ __forceinline__ void store_single(const GivenParams& p, int64_t b, int token)
+{
+    const int t = threadIdx.x;
+    if (t == 0) p.out_count[b] = token >= 0 ? 1 : 0;
+    for (int64_t n = t; n < p.N; n += NT) {
+        p.out_token[b * p.N + n] = token;
+        if (p.out_logprob) p.out_logprob[b * p.N + n] = token >= 0 ? 0.0f : __uint_as_float(0x7FC00000u);
+    }
+}
+
+// The exact cut: the logit at and above which a row's finite tokens are kept.
+// The undecided tokens are in sh.list (`listed`: `ln` places) or read from the
+// row again; kmin, kmax: this thread's least and largest key of those that
+// are in no list.  Adds the kept ones to sh.subc (or gives the one weight of
+// all, for sh.pre of each segment) and to `count`.
+template <int DT, int NT, class Shared>
+__device__ __forceinline__ float resolve_row(Shared& sh, const GivenParams& p, const void* row, const Deal& d,
+                                             const RowIn& in, const RowPlan& o, const Fixed& fx, bool listed, uint32_t ln,
+                                             uint32_t kmin, uint32_t kmax, uint32_t& count, double& one_weight)
+{
+    constexpr int GN = Group<DT>::N;
+    const int t = threadIdx.x;
+    const double scale = ldexp(1.0, p.bits), inv_scale = ldexp(1.0, -p.bits);
+    const bool cut_p = in.P < 1.0f;
+    uint32_t cut = order_key(fmaxf(o.level, kLowest));
+    one_weight = 0.0;
+    if (o.mode == kGivenCells) {
+        // Every undecided token (key, index), from the list or from memory.
+        auto undecided = [&](auto fn) {
+            const uint32_t n = listed ? ln : (uint32_t)p.V;
+#pragma unroll 1
+            for (uint32_t i = t; i < n; i += NT) {
+                float x;
+                uint32_t idx = i;
+                if (listed) {
+                    x = __uint_as_float(sh.list[i].x);  // (kEmpty is NaN)
+                    idx = sh.list[i].y;
+                } else {
+                    x = logit_at<DT>(row, i);
+                }
+                if (!(x >= o.floor_x)) continue;
+                double h;
+                const int r = rank_of(o, x, h);
+                if (r >= o.r_lo && (r <= o.r_hi || r == o.rb)) fn(x, idx, r, h);
+            }
+        };
+        // Keys that bound those of rank r's cell (a tenth of a cell to spare).
+        auto key_at = [&](int r, double off) {
+            if (r > o.top) return off < 0.0 ? 0u : 0xFFFFFFFFu;
+            return order_key((float)(((double)(o.top - r) + off - (o.c.bm - kMagic)) / o.c.s));
+        };
+        // Long runs of one value (more undecided tokens than the list holds,
+        // all of one key): they share a fate, which needs no search.
+        uint32_t one_key = 0;
+        if (!listed) {
+            for (uint32_t i = t; i < Shared::kCap; i += NT) {
+                const float x = __uint_as_float(sh.list[i].x);
+                if (!(x >= o.floor_x)) continue;
+                kmin = min(kmin, order_key(x));
+                kmax = max(kmax, order_key(x));
+            }
+            const uint64_t both = block_reduce<NT>(
+                (uint64_t)kmax << 32 | (uint32_t)~kmin,
+                [](uint64_t a, uint64_t e) {
+                    const uint64_t hi = 0xFFFFFFFF00000000ull;
+                    return ((a & hi) > (e & hi) ? a & hi : e & hi) | ((uint32_t)a > (uint32_t)e ? (uint32_t)a : (uint32_t)e);
+                },
+                sh.red64);
+            if ((uint32_t)(both >> 32) == ~(uint32_t)both) one_key = (uint32_t)(both >> 32);
+        }
+        const uint32_t from_minp = order_key(fmaxf(o.tmp, kLowest));
+        uint32_t bottom = from_minp;  // lowest key that survives min-p and top-k
+        double s_bottom = 0.0;        // mass of the bottom cell's survivors
+        // First the bottom cell by top-k (each token counts 1), then the
+        // crossing cell by top-p (each token counts its weight).
+#pragma unroll 1
+        for (int step = 0; step < 2; ++step) {
+            int cell;
+            uint64_t thr;
+            if (step == 0) {
+                if (o.rb == kRankNone) continue;
+                cell = o.rb;
+                thr = in.use_k && sh.n_above < (uint32_t)in.K ? (uint64_t)in.K - sh.n_above : 0;
+            } else {
+                if (!cut_p) break;
+                if (t == 0) {
+                    // The crossing cell: the first whose running mass reaches p S.
+                    const double want = (double)in.P * (sh.s_above + s_bottom);
+                    double a = sh.a_lo, at = sh.a_lo;
+                    int found = o.r_lo;
+#pragma unroll 1
+                    for (int r = o.r_lo; r <= o.r_hi; ++r) {
+                        const double wr =
+                            r == o.rb ? s_bottom : rank_weight(sh.root, r) * ((double)sh.hist[o.top - r] * inv_scale);
+                        if (wr > 0.0) {
+                            found = r;
+                            at = a;
+                            if (a + wr >= want) break;
+                        }
+                        a += wr;
+                    }
+                    const double q = (want - at) / (rank_weight(sh.root, found) * inv_scale);
+                    sh.cross = found;
+                    sh.tc = !(q > 1.0) ? 1 : (q < 1.8e19 ? (uint64_t)ceil(q) : ~0ull);
+                }
+                __syncthreads();
+                cell = uniform(sh.cross);
+                thr = sh.tc;
+            }
+            if (thr) {
+                uint32_t found = one_key;
+                if (!one_key) {
+                    const SelectResult r = select_level<NT>(
+                        [&](auto fn) {
+                            undecided([&](float x, uint32_t, int rank, double h) {
+                                const uint32_t key = order_key(x);
+                                if (rank == cell && key >= bottom) fn(key, step ? fx(h) : (uint64_t)1);
+                            });
+                        },
+                        [&](uint64_t) { return thr; }, sh.sel, key_at(cell, -0.6), key_at(cell, 0.6));
+                    found = r.total ? r.level : 0u;
+                }
+                bottom = max(bottom, found);
+            }
+            if (step == 0 && o.rb <= o.top && cut_p) {
+                uint64_t sum = 0;
+                if (one_key) {
+                    sum = t == 0 && one_key >= bottom ? sh.hist[o.top - o.rb] : 0;
+                } else {
+                    undecided([&](float x, uint32_t, int rank, double h) {
+                        if (rank == o.rb && order_key(x) >= bottom) sum += fx(h);
+                    });
+                }
+                sum = block_reduce<NT>(sum, SumU64(), sh.red64);
+                s_bottom = rank_weight(sh.root, o.rb) * ((double)sum * inv_scale);
+            }
+        }
+        cut = bottom;
+        if (one_key) {
+            one_weight = one_key >= cut ? mass_of(o, sh.root, key_value(one_key)) : 0.0;
+            if (one_key >= cut) count += (uint32_t)sh.pre[t];
+        } else {
+            // The kept among them, added to their segments.
+            undecided([&](float x, uint32_t idx, int, double) {
+                if (order_key(x) >= cut) {
+                    const uint32_t step = idx / (GN * kWave), own = step / d.steps;
+                    atomicAdd((unsigned long long*)&sh.subc[own * d.spw + (step - own * d.steps) / d.sps],
+                              (unsigned long long)fixed_point(mass_of(o, sh.root, x) * scale));
+                    ++count;
+                }
+            });
+        }
+        __syncthreads();
+    }
+    return key_value(cut);
+}
+
+// The draws, from sh.sub, sh.subc and sh.pre of the row's `subs` segments (no
+// more than NT) and the kept tokens' count (of each thread).  Returns the kept
+// mass.
+template <int DT, bool VEC, int NT, class Shared>
+__device__ __forceinline__ double draw_row(Shared& sh, const GivenParams& p, int64_t b, const void* row, const Deal& d,
+                                           uint32_t subs, const RowIn& in, const RowPlan& o, float low, uint32_t count,
+                                           double one_weight)
+{
+    constexpr int GN = Group<DT>::N;
+    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+    const double inv_scale = ldexp(1.0, -p.bits);
+    count = (uint32_t)block_reduce<NT>((uint64_t)count, SumU64(), sh.red64);
+    const double mine = sh.sub[t] + one_weight * sh.pre[t] + (double)sh.subc[t] * inv_scale;
+    double S;
+    const double prefix = block_exclusive_sum_f64<NT>(mine, sh.redf, S);
+    sh.sub[t] = mine > 0.0 ? prefix + mine : -1.0;
+    sh.pre[t] = prefix;
+    __syncthreads();
+    if (t == 0) p.out_count[b] = (int32_t)count;
+    for (int64_t n = w; n < p.N; n += (NT / kWave)) {
+        const double u = p.u_f64 ? ((const double*)p.uniforms)[b * p.N + n] : (double)((const float*)p.uniforms)[b * p.N + n];
+        int token = -1;
+        float xt = 0.0f;  // its logit
+        if (u == u) {
+            const double at = (u < 0.0 ? 0.0 : u) * S;
+            // The first segment whose running sum exceeds `at`.
+            uint32_t lo = 0xFFFFFFFFu;
+#pragma unroll 1
+            for (uint32_t i = 0; i < subs && lo == 0xFFFFFFFFu && u < 1.0; i += kWave) {
+                const uint64_t over = lanes(sh.sub[i + lane] > at);
+                if (over) lo = i + (uint32_t)__builtin_ctzll(over);
+            }
+            if (lo != 0xFFFFFFFFu) {
+                double run = sh.pre[lo];
+                const uint32_t own = lo / d.spw, s0 = own * d.steps + (lo - own * d.spw) * d.sps;
+                const uint32_t s1 = min(s0 + d.sps, (own + 1) * d.steps);
+                u32x4 raw[kSubSteps];
+#pragma unroll
+                for (int k = 0; k < kSubSteps; ++k)
+                    raw[k] = load_raw<DT, VEC>(row, min(s0 + k, s1 - 1) * kWave + lane, d.groups, p.V);
+                bool open = true;
+#pragma unroll 1
+                for (uint32_t i = s0; i < s1 && open; ++i) {
+                    const uint32_t g = i * kWave + lane;
+                    float x[GN];
+                    tokens_of<DT>(raw[0], g, true, p.V, x);
+#pragma unroll
+                    for (int k = 0; k + 1 < kSubSteps; ++k) raw[k] = raw[k + 1];
+                    raw[kSubSteps - 1] =
+                        load_raw<DT, VEC>(row, min(i + kSubSteps, s1 - 1) * kWave + lane, d.groups, p.V);
+                    double wg[GN], sum = 0.0;
+                    int mine_at = -1;  // this lane's last token with mass
+                    float x_at = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) {
+                        wg[j] = x[j] >= low ? mass_of(o, sh.root, x[j]) : 0.0;
+                        sum += wg[j];
+                        if (wg[j] > 0.0) {
+                            mine_at = (int)(g * GN + j);
+                            x_at = x[j];
+                        }
+                    }
+                    double all;
+                    const double inc = wave_inclusive_sum(sum, all);
+                    const double prev = wave_shift_up1(inc);
+                    const uint64_t hit = lanes(run + inc > at && mine_at >= 0), any = lanes(mine_at >= 0);
+                    if (hit) {
+                        // The first of the lane's tokens past `at`.
+                        double a = run + (lane ? prev : 0.0);
+                        bool here = true;
+#pragma unroll
+                        for (int j = 0; j < GN; ++j) {
+                            a += wg[j];
+                            if (here && a > at && wg[j] > 0.0) {
+                                mine_at = (int)(g * GN + j);
+                                x_at = x[j];
+                                here = false;
+                            }
+                        }
+                    }
+                    if (any) {  // the lane that holds it, or so far the last with mass
+                        const int L = hit ? (int)__builtin_ctzll(hit) : 63 - (int)__builtin_clzll(any);
+                        token = __builtin_amdgcn_readlane(mine_at, L);
+                        xt = lane_value(x_at, L);
+                    }
+                    open = !hit;
+                    run += all;
+                }
+            } else {
+                // At or past the end: the row's last kept token of positive weight.
+#pragma unroll 1
+                for (int64_t i = (int64_t)((d.groups + kWave - 1) / kWave) - 1; i >= 0 && token < 0; --i) {
+                    const uint32_t g = (uint32_t)i * kWave + lane;
+                    float x[GN], x_at = 0.0f;
+                    tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
+                    int mine_at = -1;
+#pragma unroll
+                    for (int j = 0; j < GN; ++j)
+                        if (x[j] >= low && weight_of(o, sh.root, x[j]) > 0.0) {
+                            mine_at = (int)(g * GN + j);
+                            x_at = x[j];
+                        }
+                    const uint64_t any = lanes(mine_at >= 0);
+                    if (any) {
+                        const int L = 63 - (int)__builtin_clzll(any);
+                        token = __builtin_amdgcn_readlane(mine_at, L);
+                        xt = lane_value(x_at, L);
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            p.out_token[b * p.N + n] = token;
+            if (p.out_logprob) {
+                float lp = __uint_as_float(0x7FC00000u);
+                if (token >= 0)
+                    // (the mass is measured from the max's cell, not from the max itself)
+                    lp = (float)(((double)xt - (double)o.m) / (double)in.T - (log(S) - o.hm * (kLn2 / kOctave)));
+                p.out_logprob[b * p.N + n] = lp;
+            }
+        }
+    }
+    return S;
+}
+
+// One row on one workgroup.
+template <int DT, bool VEC, int NT, class Shared>
+__device__ __forceinline__ void whole_row(Shared& sh, const GivenParams& p, int64_t b)
+{
+    constexpr int GN = Group<DT>::N;
+    constexpr uint32_t kCap = Shared::kCap;
+    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+    const void* row = row_of<DT>(p, b);
+    const Deal d = deal_out<DT, NT>(p.V);
+    const Fixed fx(ldexp(1.0, p.bits));
+    const RowIn in = row_in(p, b);
+
+    if (t < kOctave) sh.root[t] = kRoot[t];
+    sh.sub[t] = 0.0;
+    sh.pre[t] = 0.0;
+    sh.subc[t] = 0;
+    if (t == 0) sh.list_n = 0;
+
+    // ---- pass 1: max, NaN / +inf, histogram -----------------------------
+    Cells c = {};
+    FirstPass f;
+    float anchor = -INFINITY;
+    if (in.want_hist) {
+        // The anchor: the max of every thread's first group.
+        float x[GN];
+        const uint32_t g = (uint32_t)w * d.steps * kWave + lane;
+        tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
+#pragma unroll
+        for (int j = 0; j < GN; ++j) anchor = fmaxf(anchor, x[j]);
+        for (int i = t; i < kSlots; i += NT) {
+            sh.hist[i] = sh.hist[kCopy + i] = 0;
+            sh.cnt[i] = 0;
+        }
+        anchor = uniform(block_reduce<NT>(anchor, MaxF32(), (float*)sh.redf));
+    }
+    float m = -INFINITY;
+    bool hist = in.want_hist && anchor > -INFINITY && anchor < INFINITY;
+    // At most three turns: for the max alone where the first tokens were all
+    // masked, with a histogram, and once more where the max lay above its window.
+#pragma unroll 1
+    for (int turn = 0; turn < 3; ++turn) {
+        if (hist) c = make_cells(anchor, in.T);
+        if (!hist)
+            f = first_pass<DT, VEC, kPassMax, false>(row, d, p.V, c, fx, sh);
+        else if (in.use_k && c.fast)
+            f = first_pass<DT, VEC, kPassCount, true>(row, d, p.V, c, fx, sh);
+        else if (in.use_k)
+            f = first_pass<DT, VEC, kPassCount, false>(row, d, p.V, c, fx, sh);
+        else if (c.fast)
+            f = first_pass<DT, VEC, kPassHist, true>(row, d, p.V, c, fx, sh);
+        else
+            f = first_pass<DT, VEC, kPassHist, false>(row, d, p.V, c, fx, sh);
+        m = uniform(block_reduce<NT>(
+            f.m, [](float a, float e) { return __builtin_elementwise_maximum(a, e); }, (float*)sh.redf));
+        if (!in.want_hist || !(m > -INFINITY && m < INFINITY)) break;
+        double h;
+        if (hist && uniform(slot_of(c, m, h)) < kSlots) break;
+        // Anchored at the row's own max, no token lies above the window.
+        anchor = m;
+        if (hist) {
+            for (int i = t; i < kSlots; i += NT) {
+                sh.hist[i] = sh.hist[kCopy + i] = 0;
+                sh.cnt[i] = 0;
+            }
+            __syncthreads();
+        }
+        hist = true;
+    }
+
+    if (row_error(in, m) || in.greedy) {
+        int token = -1;
+        if (!row_error(in, m)) {
+            // The lowest index that holds the max: every thread knows the step
+            // that first held its own.
+            uint32_t first = 0xFFFFFFFFu;
+            if (f.m == m) {
+                const uint32_t g = ((uint32_t)w * d.steps + f.at) * kWave + lane;
+                float x[GN];
+                tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
+#pragma unroll
+                for (int j = GN - 1; j >= 0; --j)
+                    if (x[j] == m) first = g * GN + j;
+            }
+            token = (int)block_reduce<NT>(first, MinU32(), (uint32_t*)sh.red64);
+        }
+        store_single<NT>(p, b, token);
+        if (p.out_probs)
+            for (int64_t i = t; i < p.V; i += NT) p.out_probs[b * p.V + i] = i == token ? 1.0f : 0.0f;
+        return;
+    }
+    uint32_t finite = 0;
+    if (in.use_k) finite = (uint32_t)block_reduce<NT>((uint64_t)(lane == 0 ? f.finite : 0), SumU64(), sh.red64);
+
+    // ---- the cells of the cuts -------------------------------------------
+    const RowPlan o = plan_row<NT>(sh, in, c, m, finite, true, p.bits);
 
     // ---- pass 2: masses of the surely kept, list of the undecided -----------
-    // Slots above s_sure (kGivenLevel: tokens from floor_x up) are surely kept;
+    // Slots above s_sure (kGivenLevel: tokens from o.floor_x up) are surely kept;
     // those from s_und to it, and s_bot where it is apart from them, undecided.
-    const int s_sure = mode == kGivenLevel || r_lo > top ? -1 : top - r_lo;
-    const int s_und = r_hi > top ? 0 : top - r_hi, s_bot = top - rb;
-    const bool apart = mode == kGivenCells && rb <= top && rb > r_hi;
-    const bool below = mode == kGivenCells && rb == top + 1;  // the undecided are those below the window
+    const int s_sure = o.mode == kGivenLevel || o.r_lo > o.top ? -1 : o.top - o.r_lo;
+    const int s_und = o.r_hi > o.top ? 0 : o.top - o.r_hi, s_bot = o.top - o.rb;
+    const bool apart = o.mode == kGivenCells && o.rb <= o.top && o.rb > o.r_hi;
+    const bool below = o.mode == kGivenCells && o.rb == o.top + 1;  // the undecided are those below the window
     double* const cell_mass = (double*)(sh.hist + kCopy);
     for (int i = t; i <= kSlots; i += NT)
-        cell_mass[i] = i > s_sure && i <= top ? rank_weight(sh.root, top - i) : 0.0;
+        cell_mass[i] = i > s_sure && i <= o.top ? rank_weight(sh.root, o.top - i) : 0.0;
     __syncthreads();
     uint32_t count = 0;                     // kept tokens, of each lane and of lane 0's wave
     uint32_t kmin = 0xFFFFFFFFu, kmax = 0;  // keys of the undecided that are not listed
@@ -829,18 +1177,18 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
                 seg_left = d.sps;
             }
         };
-        if (mode == kGivenLevel && c.fast) {
+        if (o.mode == kGivenLevel && o.c.fast) {
             stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t, const float (&x)[GN]) {
                 double e[GN], q[GN], h[GN];
                 float xc[GN];
                 int sl[GN];
 #pragma unroll
                 for (int j = 0; j < GN; ++j) {
-                    const bool in = x[j] >= floor_x;
-                    xc[j] = fmaxf(in ? x[j] : c.lo, c.lo);
+                    const bool in = x[j] >= o.floor_x;
+                    xc[j] = fmaxf(in ? x[j] : o.c.lo, o.c.lo);
                     sure_n += (uint32_t)__builtin_popcountll(lanes(in));
                 }
-                slots_of<GN, true>(c, xc, sl, h);
+                slots_of<GN, true>(o.c, xc, sl, h);
 #pragma unroll
                 for (int j = 0; j < GN; ++j) e[j] = cell_mass[min((uint32_t)sl[j], (uint32_t)kSlots)];
                 in_cells(h, q);
@@ -848,14 +1196,14 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
                 for (int j = 0; j < GN; ++j) acc[j & 1] = fma(e[j], q[j], acc[j & 1]);
                 end_step(i);
             });
-        } else if (c.fast && !below) {
-            // (a token below floor_x falls into a slot of no mass below s_und)
-            const float from = fmaxf(floor_x, c.lo);
+        } else if (o.c.fast && !below) {
+            // (a token below o.floor_x falls into a slot of no mass below s_und)
+            const float from = fmaxf(o.floor_x, o.c.lo);
             stream_row<DT, VEC>(row, d, p.V, [&](uint32_t i, uint32_t g, const float (&x)[GN]) {
                 float most = x[0];
 #pragma unroll
                 for (int j = 1; j < GN; ++j) most = fmaxf(most, x[j]);
-                if (lanes(most >= floor_x)) {  // uniform: most steps of many rows hold no such token
+                if (lanes(most >= o.floor_x)) {  // uniform: most steps of many rows hold no such token
                     uint64_t some[GN];
                     uint32_t n = 0;
                     double e[GN], q[GN], h[GN];
@@ -863,7 +1211,7 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
                     int sl[GN];
 #pragma unroll
                     for (int j = 0; j < GN; ++j) xc[j] = fmaxf(x[j], from);
-                    slots_of<GN, true>(c, xc, sl, h);
+                    slots_of<GN, true>(o.c, xc, sl, h);
 #pragma unroll
                     for (int j = 0; j < GN; ++j) e[j] = cell_mass[min((uint32_t)sl[j], (uint32_t)kSlots)];
                     in_cells(h, q);
@@ -891,13 +1239,13 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
 #pragma unroll
                 for (int j = 0; j < GN; ++j) {
                     double h;  // (finite tokens only: a -inf here would make the sum NaN)
-                    const bool in = x[j] >= floor_x;
-                    const int sl = slot_of(c, fmaxf(x[j], floor_x), h);
-                    const bool sure = mode == kGivenLevel ? in : in & (sl > s_sure);
+                    const bool in = x[j] >= o.floor_x;
+                    const int sl = slot_of(o.c, fmaxf(x[j], o.floor_x), h);
+                    const bool sure = o.mode == kGivenLevel ? in : in & (sl > s_sure);
                     if (sure & (sl >= 0)) acc[0] = fma(cell_mass[min(sl, kSlots)], in_cell(h), acc[0]);
                     sure_n += (uint32_t)__builtin_popcountll(lanes(sure));
                     const bool und = below ? sl < 0 : (sl >= s_und) | (apart & (sl == s_bot));
-                    some[j] = mode == kGivenLevel ? 0 : lanes(in & !sure & und);
+                    some[j] = o.mode == kGivenLevel ? 0 : lanes(in & !sure & und);
                     n += (uint32_t)__builtin_popcountll(some[j]);
                 }
                 if (n) put(x, some, n, g);  // uniform
@@ -910,253 +1258,13 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
     __syncthreads();
 
     // ---- the exact cut level ---------------------------------------------
-    uint32_t cut = order_key(fmaxf(level, lowest));
-    double one_weight = 0.0;  // every undecided token is kept, with this weight
-    if (mode == kGivenCells) {
-        const uint32_t ln = sh.list_n;
-        const bool listed = ln <= kCap;
-        // Every undecided token (key, index), from the list or from memory.
-        auto undecided = [&](auto fn) {
-            const uint32_t n = listed ? ln : (uint32_t)p.V;
-#pragma unroll 1
-            for (uint32_t i = t; i < n; i += NT) {
-                float x;
-                uint32_t idx = i;
-                if (listed) {
-                    x = __uint_as_float(sh.list[i].x);  // (kEmpty is NaN)
-                    idx = sh.list[i].y;
-                } else {
-                    x = logit_at<DT>(row, i);
-                }
-                if (!(x >= floor_x)) continue;
-                double h;
-                const int r = rank_of(x, h);
-                if (r >= r_lo && (r <= r_hi || r == rb)) fn(x, idx, r, h);
-            }
-        };
-        // Keys that bound those of rank r's cell (a tenth of a cell to spare).
-        auto key_at = [&](int r, double off) {
-            if (r > top) return off < 0.0 ? 0u : 0xFFFFFFFFu;
-            return order_key((float)(((double)(top - r) + off - (c.bm - kMagic)) / c.s));
-        };
-        // Long runs of one value (more undecided tokens than the list holds,
-        // all of one key): they share a fate, which needs no search.
-        uint32_t one_key = 0;
-        if (!listed) {
-            for (uint32_t i = t; i < kCap; i += NT) {
-                const float x = __uint_as_float(sh.list[i].x);
-                if (!(x >= floor_x)) continue;
-                kmin = min(kmin, order_key(x));
-                kmax = max(kmax, order_key(x));
-            }
-            const uint64_t both = block_reduce<NT>(
-                (uint64_t)kmax << 32 | (uint32_t)~kmin,
-                [](uint64_t a, uint64_t e) {
-                    const uint64_t hi = 0xFFFFFFFF00000000ull;
-                    return ((a & hi) > (e & hi) ? a & hi : e & hi) | ((uint32_t)a > (uint32_t)e ? (uint32_t)a : (uint32_t)e);
-                },
-                sh.red64);
-            if ((uint32_t)(both >> 32) == ~(uint32_t)both) one_key = (uint32_t)(both >> 32);
-        }
-        const uint32_t from_minp = order_key(fmaxf(tmp, lowest));
-        uint32_t bottom = from_minp;  // lowest key that survives min-p and top-k
-        double s_bottom = 0.0;        // mass of the bottom cell's survivors
-        // First the bottom cell by top-k (each token counts 1), then the
-        // crossing cell by top-p (each token counts its weight).
-#pragma unroll 1
-        for (int step = 0; step < 2; ++step) {
-            int cell;
-            uint64_t thr;
-            if (step == 0) {
-                if (rb == kRankNone) continue;
-                cell = rb;
-                thr = use_k && sh.n_above < (uint32_t)K ? (uint64_t)K - sh.n_above : 0;
-            } else {
-                if (!cut_p) break;
-                if (t == 0) {
-                    // The crossing cell: the first whose running mass reaches p S.
-                    const double want = (double)P * (sh.s_above + s_bottom);
-                    double a = sh.a_lo, at = sh.a_lo;
-                    int found = r_lo;
-#pragma unroll 1
-                    for (int r = r_lo; r <= r_hi; ++r) {
-                        const double wr =
-                            r == rb ? s_bottom : rank_weight(sh.root, r) * ((double)sh.hist[top - r] * inv_scale);
-                        if (wr > 0.0) {
-                            found = r;
-                            at = a;
-                            if (a + wr >= want) break;
-                        }
-                        a += wr;
-                    }
-                    const double q = (want - at) / (rank_weight(sh.root, found) * inv_scale);
-                    sh.cross = found;
-                    sh.tc = !(q > 1.0) ? 1 : (q < 1.8e19 ? (uint64_t)ceil(q) : ~0ull);
-                }
-                __syncthreads();
-                cell = uniform(sh.cross);
-                thr = sh.tc;
-            }
-            if (thr) {
-                uint32_t found = one_key;
-                if (!one_key) {
-                    const SelectResult r = select_level<NT>(
-                        [&](auto fn) {
-                            undecided([&](float x, uint32_t, int rank, double h) {
-                                const uint32_t key = order_key(x);
-                                if (rank == cell && key >= bottom) fn(key, step ? fx(h) : (uint64_t)1);
-                            });
-                        },
-                        [&](uint64_t) { return thr; }, sh.sel, key_at(cell, -0.6), key_at(cell, 0.6));
-                    found = r.total ? r.level : 0u;
-                }
-                bottom = max(bottom, found);
-            }
-            if (step == 0 && rb <= top && cut_p) {
-                uint64_t sum = 0;
-                if (one_key) {
-                    sum = t == 0 && one_key >= bottom ? sh.hist[top - rb] : 0;
-                } else {
-                    undecided([&](float x, uint32_t, int rank, double h) {
-                        if (rank == rb && order_key(x) >= bottom) sum += fx(h);
-                    });
-                }
-                sum = block_reduce<NT>(sum, SumU64(), sh.red64);
-                s_bottom = rank_weight(sh.root, rb) * ((double)sum * inv_scale);
-            }
-        }
-        cut = bottom;
-        if (one_key) {
-            one_weight = one_key >= cut ? mass_of(key_value(one_key)) : 0.0;
-            if (one_key >= cut) count += (uint32_t)sh.pre[t];
-        } else {
-            // The kept among them, added to their segments.
-            undecided([&](float x, uint32_t idx, int, double) {
-                if (order_key(x) >= cut) {
-                    const uint32_t step = idx / (GN * kWave), own = step / d.steps;
-                    atomicAdd((unsigned long long*)&sh.subc[own * d.spw + (step - own * d.steps) / d.sps],
-                              (unsigned long long)fixed_point(mass_of(x) * scale));
-                    ++count;
-                }
-            });
-        }
-        __syncthreads();
-    }
-    const float low = key_value(cut);  // kept: finite and x >= low
+    double one_weight;
+    const float low =
+        resolve_row<DT, NT>(sh, p, row, d, in, o, fx, sh.list_n <= kCap, sh.list_n, kmin, kmax, count, one_weight);
 
     // ---- the draws ---------------------------------------------------------
-    count = (uint32_t)block_reduce<NT>((uint64_t)count, SumU64(), sh.red64);
-    const uint32_t subs = d.spw * kWaves;
-    const double mine = sh.sub[t] + one_weight * sh.pre[t] + (double)sh.subc[t] * inv_scale;
-    double S;
-    const double prefix = block_exclusive_sum_f64<NT>(mine, sh.redf, S);
-    sh.sub[t] = mine > 0.0 ? prefix + mine : -1.0;
-    sh.pre[t] = prefix;
-    __syncthreads();
-    if (t == 0) p.out_count[b] = (int32_t)count;
-    for (int64_t n = w; n < p.N; n += kWaves) {
-        const double u = p.u_f64 ? ((const double*)p.uniforms)[b * p.N + n] : (double)((const float*)p.uniforms)[b * p.N + n];
-        int token = -1;
-        float xt = 0.0f;  // its logit
-        if (u == u) {
-            const double at = (u < 0.0 ? 0.0 : u) * S;
-            // The first segment whose running sum exceeds `at`.
-            uint32_t lo = 0xFFFFFFFFu;
-#pragma unroll 1
-            for (uint32_t i = 0; i < subs && lo == 0xFFFFFFFFu && u < 1.0; i += kWave) {
-                const uint64_t over = lanes(sh.sub[i + lane] > at);
-                if (over) lo = i + (uint32_t)__builtin_ctzll(over);
-            }
-            if (lo != 0xFFFFFFFFu) {
-                double run = sh.pre[lo];
-                const uint32_t own = lo / d.spw, s0 = own * d.steps + (lo - own * d.spw) * d.sps;
-                const uint32_t s1 = min(s0 + d.sps, (own + 1) * d.steps);
-                u32x4 raw[kSubSteps];
-#pragma unroll
-                for (int k = 0; k < kSubSteps; ++k)
-                    raw[k] = load_raw<DT, VEC>(row, min(s0 + k, s1 - 1) * kWave + lane, d.groups, p.V);
-                bool open = true;
-#pragma unroll 1
-                for (uint32_t i = s0; i < s1 && open; ++i) {
-                    const uint32_t g = i * kWave + lane;
-                    float x[GN];
-                    tokens_of<DT>(raw[0], g, true, p.V, x);
-#pragma unroll
-                    for (int k = 0; k + 1 < kSubSteps; ++k) raw[k] = raw[k + 1];
-                    raw[kSubSteps - 1] =
-                        load_raw<DT, VEC>(row, min(i + kSubSteps, s1 - 1) * kWave + lane, d.groups, p.V);
-                    double wg[GN], sum = 0.0;
-                    int mine_at = -1;  // this lane's last token with mass
-                    float x_at = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < GN; ++j) {
-                        wg[j] = x[j] >= low ? mass_of(x[j]) : 0.0;
-                        sum += wg[j];
-                        if (wg[j] > 0.0) {
-                            mine_at = (int)(g * GN + j);
-                            x_at = x[j];
-                        }
-                    }
-                    double all;
-                    const double inc = wave_inclusive_sum(sum, all);
-                    const double prev = wave_shift_up1(inc);
-                    const uint64_t hit = lanes(run + inc > at && mine_at >= 0), any = lanes(mine_at >= 0);
-                    if (hit) {
-                        // The first of the lane's tokens past `at`.
-                        double a = run + (lane ? prev : 0.0);
-                        bool here = true;
-#pragma unroll
-                        for (int j = 0; j < GN; ++j) {
-                            a += wg[j];
-                            if (here && a > at && wg[j] > 0.0) {
-                                mine_at = (int)(g * GN + j);
-                                x_at = x[j];
-                                here = false;
-                            }
-                        }
-                    }
-                    if (any) {  // the lane that holds it, or so far the last with mass
-                        const int L = hit ? (int)__builtin_ctzll(hit) : 63 - (int)__builtin_clzll(any);
-                        token = __builtin_amdgcn_readlane(mine_at, L);
-                        xt = lane_value(x_at, L);
-                    }
-                    open = !hit;
-                    run += all;
-                }
-            } else {
-                // At or past the end: the row's last kept token of positive weight.
-#pragma unroll 1
-                for (int64_t i = (int64_t)kWaves * d.steps - 1; i >= 0 && token < 0; --i) {
-                    const uint32_t g = (uint32_t)i * kWave + lane;
-                    float x[GN], x_at = 0.0f;
-                    tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
-                    int mine_at = -1;
-#pragma unroll
-                    for (int j = 0; j < GN; ++j)
-                        if (x[j] >= low && weight_of(x[j]) > 0.0) {
-                            mine_at = (int)(g * GN + j);
-                            x_at = x[j];
-                        }
-                    const uint64_t any = lanes(mine_at >= 0);
-                    if (any) {
-                        const int L = 63 - (int)__builtin_clzll(any);
-                        token = __builtin_amdgcn_readlane(mine_at, L);
-                        xt = lane_value(x_at, L);
-                    }
-                }
-            }
-        }
-        if (lane == 0) {
-            p.out_token[b * p.N + n] = token;
-            if (p.out_logprob) {
-                float lp = __uint_as_float(0x7FC00000u);
-                if (token >= 0)
-                    // (the mass is measured from the max's cell, not from the max itself)
-                    lp = (float)(((double)xt - (double)m) / (double)T - (log(S) - hm * (kLn2 / kOctave)));
-                p.out_logprob[b * p.N + n] = lp;
-            }
-        }
-    }
+    const double S =
+        draw_row<DT, VEC, NT>(sh, p, b, row, d, d.spw * Shared::kWaves, in, o, low, count, one_weight);
 
     // ---- the distribution ---------------------------------------------------
     if (p.out_probs) {
@@ -1174,7 +1282,7 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
             if (lanes(any)) {
 #pragma unroll
                 for (int j = 0; j < GN; ++j)
-                    if (x[j] >= low) q[j] = (float)(weight_of(x[j]) * inv);
+                    if (x[j] >= low) q[j] = (float)(weight_of(o, sh.root, x[j]) * inv);
             }
             const int64_t i0 = (int64_t)g * GN;
             if (vec && i0 + GN <= p.V) {
@@ -1186,6 +1294,519 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
                     if (i0 + j < p.V) out[i0 + j] = q[j];
             }
         });
+    }
+}
+
+template <int DT, bool VEC, int NT>
+__global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
+{
+    __shared__ GivenShared<NT> sh;
+    whole_row<DT, VEC, NT>(sh, p, blockIdx.x);
+}
+
+// ---------------------------------------------------------------------------
+// Rows split over workgroups.  A part is 32 KB of a row, held in the registers
+// of one 256-thread workgroup; four launches (five with the distribution):
+//
+//   given_hist_kernel   per part: max and histogram, over a lattice anchored
+//                       at the max of 256 groups spread over the whole row
+//                       (every part of a row reads the same ones)
+//   given_plan_kernel   per row: joins the histograms, finds the cells of the cuts
+//   given_mass_kernel   per part: masses of the surely kept tokens per segment,
+//                       list of the undecided
+//   given_draw_kernel   per row: exact cut, draws
+//   given_probs_kernel  per part: probabilities
+//
+// Launch boundaries are the only joins, so nothing waits inside a kernel and
+// the workspace needs no initial value.  What a part cannot do for itself
+// (a max above the window, a window that reaches past the finite logits, a
+// top-k cut below the window) is left to one workgroup, which runs the
+// unsplit row in given_draw_kernel.
+// ---------------------------------------------------------------------------
+constexpr int kPartThreads = 256;
+constexpr int kPartWaves = kPartThreads / kWave;
+constexpr int kPartSteps = 8;                                        // groups of a lane
+constexpr int kPartSegs = kPartWaves * kPartSteps / kSubSteps;       // segments
+constexpr int kPartCap = 1024;                                       // listed tokens
+constexpr int kMaxParts = 64;                                        // of a row: its segments fit one per thread
+constexpr int kDrawThreads = 512;
+static_assert(kMaxParts * kPartSegs <= kDrawThreads, "one segment per thread of given_draw_kernel");
+
+template <int DT>
+constexpr int part_tokens() { return kPartThreads * kPartSteps * Group<DT>::N; }
+
+struct PartHead {  // given_hist_kernel
+    float anchor, m;
+    uint32_t finite, first;  // top-k rows: tokens above -inf; greedy rows: lowest index of m
+    int lo, hi;              // its slots of the histogram are lo .. hi
+    int ok;                  // the lattice is a fast one
+    int pad;
+};
+struct PartTail {  // given_mass_kernel
+    uint32_t listed, sure, kmin, kmax;
+};
+struct RowState {
+    RowPlan o;
+    double s_above, a_lo, S;
+    float low;
+    uint32_t n_above;
+    int token;  // kGivenGreedy, kGivenError
+};
+
+struct GivenWork {
+    RowState* state;   // [B]
+    PartHead* head;    // [B][C]
+    PartTail* tail;    // [B][C]
+    uint64_t* hist;    // [B][C][kSlots]; part 0's holds the joined cells of the cuts after given_plan_kernel
+    uint32_t* cnt;     // [B][C][kSlots]
+    double* sub;       // [B][C][kPartSegs]
+    uint32_t* und;     // [B][C][kPartSegs]
+    uint2* list;       // [B][C][kPartCap]
+    int C;
+};
+
+// The groups of this part in registers: step i of wave w is group
+// (part 32 + w 8 + i) 64 + lane of the row.
+template <int DT, bool VEC>
+__device__ __forceinline__ uint32_t load_part(const void* row, int part, uint32_t groups, int64_t V,
+                                              u32x4 (&raw)[kPartSteps])
+{
+    const uint32_t g0 = ((uint32_t)part * kPartWaves + uniform(threadIdx.x / kWave)) * kPartSteps * kWave;
+#pragma unroll
+    for (int i = 0; i < kPartSteps; ++i)
+        raw[i] = load_raw<DT, VEC>(row, g0 + i * kWave + (threadIdx.x & (kWave - 1)), groups, V);
+    return g0;
+}
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kPartThreads) void given_hist_kernel(GivenParams p, GivenWork wk)
+{
+    constexpr int GN = Group<DT>::N;
+    __shared__ uint64_t hist[kSlots + kWave];
+    __shared__ uint32_t cnt[kSlots + kWave];
+    __shared__ uint64_t red[kPartWaves];
+    const int t = threadIdx.x, lane = t & (kWave - 1);
+    const int64_t b = blockIdx.x / (uint32_t)wk.C;
+    const int part = (int)(blockIdx.x % (uint32_t)wk.C);
+    const void* row = row_of<DT>(p, b);
+    const uint32_t groups = (uint32_t)((p.V + GN - 1) / GN), whole = (uint32_t)(p.V / GN);
+    const RowIn in = row_in(p, b);
+    u32x4 raw[kPartSteps];
+    const uint32_t g0 = load_part<DT, VEC>(row, part, groups, p.V, raw);
+    float anchor = -INFINITY;
+    if (in.want_hist) {
+        float x[GN];
+        const uint32_t g = (uint32_t)((uint64_t)groups * t / kPartThreads);
+        tokens_of<DT>(load_raw<DT, VEC>(row, g, groups, p.V), g, true, p.V, x);
+#pragma unroll
+        for (int j = 0; j < GN; ++j) anchor = fmaxf(anchor, x[j]);
+        for (int i = t; i < kSlots; i += kPartThreads) hist[i] = 0;
+        if (in.use_k)
+            for (int i = t; i < kSlots; i += kPartThreads) cnt[i] = 0;
+        anchor = uniform(block_reduce<kPartThreads>(anchor, MaxF32(), (float*)red));
+    }
+    Cells c = {};
+    if (anchor > -INFINITY && anchor < INFINITY) c = make_cells(anchor, in.T);
+    const Fixed fx(ldexp(1.0, p.bits));
+    float m = -INFINITY;
+    uint32_t finite = 0;
+    const uint32_t outside = kSlots + lane;
+    // fn(step, group, tokens)
+    auto each = [&](auto fn) {
+#pragma unroll
+        for (int i = 0; i < kPartSteps; ++i) {
+            const uint32_t g = g0 + i * kWave;
+            if (g >= groups) break;  // uniform
+            float x[GN];
+            tokens_of<DT>(raw[i], g + lane, g + kWave > whole, p.V, x);
+            fn(g + lane, x);
+        }
+    };
+    auto bin = [&](const float (&x)[GN], auto count) {
+        float xc[GN];
+        int sl[GN];
+        double h[GN];
+        uint64_t q[GN];
+#pragma unroll
+        for (int j = 0; j < GN; ++j) xc[j] = fmaxf(x[j], c.lo);
+        slots_of<GN, true>(c, xc, sl, h);
+        fx(h, q);
+#pragma unroll
+        for (int j = 0; j < GN; ++j) {
+            const uint32_t at = min((uint32_t)sl[j], outside);
+            atomicAdd((unsigned long long*)&hist[at], (unsigned long long)q[j]);
+            if constexpr (count.value) {
+                atomicAdd(&cnt[at], 1u);
+                finite += (uint32_t)__builtin_popcountll(lanes(x[j] > -INFINITY));
+            }
+        }
+    };
+    auto most = [&](const float (&x)[GN]) {
+#pragma unroll
+        for (int j = 0; j < GN; ++j) m = __builtin_elementwise_maximum(m, x[j]);
+    };
+    if (c.fast && in.use_k)
+        each([&](uint32_t, const float (&x)[GN]) {
+            most(x);
+            bin(x, std::true_type());
+        });
+    else if (c.fast)
+        each([&](uint32_t, const float (&x)[GN]) {
+            most(x);
+            bin(x, std::false_type());
+        });
+    else
+        each([&](uint32_t, const float (&x)[GN]) { most(x); });
+    m = uniform(block_reduce<kPartThreads>(
+        m, [](float a, float e) { return __builtin_elementwise_maximum(a, e); }, (float*)red));
+    PartHead o = {anchor, m, 0, 0xFFFFFFFFu, 1, 0, c.fast, 0};
+    if (in.greedy) {
+        uint32_t first = 0xFFFFFFFFu;
+        each([&](uint32_t g, const float (&x)[GN]) {
+#pragma unroll
+            for (int j = GN - 1; j >= 0; --j)
+                if (x[j] == m) first = min(first, g * GN + j);
+        });
+        o.first = block_reduce<kPartThreads>(first, MinU32(), (uint32_t*)red);
+    } else if (c.fast) {
+        if (in.use_k) o.finite = (uint32_t)block_reduce<kPartThreads>((uint64_t)(lane == 0 ? finite : 0), SumU64(), red);
+        // Its slots: from the lowest in use to the max's.
+        double h;
+        const int hi = min(uniform(slot_of(c, m, h)), kSlots - 1);
+        int lo = kSlots;
+        for (int i = t; i <= hi; i += kPartThreads)
+            if (lo == kSlots && hist[i]) lo = i;
+        lo = block_reduce<kPartThreads>(lo, MinI(), (int*)red);
+        const size_t at = ((size_t)b * wk.C + part) * kSlots;
+        for (int i = lo + t; i <= hi; i += kPartThreads) wk.hist[at + i] = hist[i];
+        if (in.use_k)
+            for (int i = lo + t; i <= hi; i += kPartThreads) wk.cnt[at + i] = cnt[i];
+        o.lo = lo;
+        o.hi = hi;
+    }
+    if (t == 0) wk.head[b * wk.C + part] = o;
+}
+
+template <int NT>
+__global__ __launch_bounds__(NT) void given_plan_kernel(GivenParams p, GivenWork wk)
+{
+    typedef GivenShared<NT> Shared;
+    __shared__ Shared sh;
+    __shared__ int s_lo[kMaxParts], s_hi[kMaxParts];
+    const int t = threadIdx.x;
+    const int64_t b = blockIdx.x;
+    const RowIn in = row_in(p, b);
+    const PartHead* head = wk.head + b * wk.C;
+    PartHead mine = {-INFINITY, -INFINITY, 0, 0xFFFFFFFFu, 1, 0, 1, 0};
+    if (t < wk.C) {
+        mine = head[t];
+        s_lo[t] = mine.lo;
+        s_hi[t] = mine.hi;
+    }
+    if (t < kOctave) sh.root[t] = kRoot[t];
+    const float m = uniform(block_reduce<NT>(
+        mine.m, [](float a, float e) { return __builtin_elementwise_maximum(a, e); }, (float*)sh.redf));
+    RowState& st = wk.state[b];
+    if (row_error(in, m) || in.greedy) {
+        const uint32_t first = block_reduce<NT>(mine.m == m ? mine.first : 0xFFFFFFFFu, MinU32(), (uint32_t*)sh.red64);
+        if (t == 0) {
+            st.o.mode = row_error(in, m) ? kGivenError : kGivenGreedy;
+            st.token = row_error(in, m) ? -1 : (int)first;
+        }
+        return;
+    }
+    Cells c = {};
+    uint32_t finite = 0;
+    bool alone = false;
+    if (in.want_hist) {
+        alone = !head[0].ok;
+        if (!alone) {
+            c = make_cells(uniform(head[0].anchor), in.T);
+            double h;
+            alone = uniform(slot_of(c, m, h)) >= kSlots;
+        }
+        if (!alone) {
+            if (in.use_k) finite = (uint32_t)block_reduce<NT>((uint64_t)mine.finite, SumU64(), sh.red64);
+            const uint64_t* hist = wk.hist + (size_t)b * wk.C * kSlots;
+            const uint32_t* cnt = wk.cnt + (size_t)b * wk.C * kSlots;
+            for (int sl = t; sl < kSlots; sl += NT) {
+                uint64_t h = 0;
+                uint32_t n = 0;
+#pragma unroll 8
+                for (int i = 0; i < wk.C; ++i)
+                    if (sl >= s_lo[i] && sl <= s_hi[i]) h += hist[(size_t)i * kSlots + sl];
+                if (in.use_k)
+#pragma unroll 8
+                    for (int i = 0; i < wk.C; ++i)
+                        if (sl >= s_lo[i] && sl <= s_hi[i]) n += cnt[(size_t)i * kSlots + sl];
+                sh.hist[sl] = h;
+                sh.cnt[sl] = n;
+            }
+        }
+    }
+    __syncthreads();
+    if (alone) {
+        if (t == 0) st.o.mode = kGivenAlone;
+        return;
+    }
+    RowPlan o = plan_row<NT>(sh, in, c, m, finite, false, p.bits);
+    if (!o.c.fast || (o.mode == kGivenCells && o.rb == o.top + 1)) o.mode = kGivenAlone;
+    __syncthreads();
+    if (o.mode == kGivenCells) {
+        uint64_t* joined = wk.hist + (size_t)b * wk.C * kSlots;
+        for (int r = o.r_lo + t; r <= o.r_hi; r += NT) joined[o.top - r] = sh.hist[o.top - r];
+        if (t == 0 && o.rb <= o.top) joined[o.top - o.rb] = sh.hist[o.top - o.rb];
+    }
+    if (t == 0) {
+        st.o = o;
+        st.s_above = sh.s_above;
+        st.a_lo = sh.a_lo;
+        st.n_above = sh.n_above;
+    }
+}
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kPartThreads) void given_mass_kernel(GivenParams p, GivenWork wk)
+{
+    constexpr int GN = Group<DT>::N;
+    __shared__ double cell_mass[kSlots + 1];
+    __shared__ double root[kOctave];
+    __shared__ uint32_t list_n, sure_all, kmin_all, kmax_all;
+    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+    const int64_t b = blockIdx.x / (uint32_t)wk.C;
+    const int part = (int)(blockIdx.x % (uint32_t)wk.C);
+    const RowPlan o = wk.state[b].o;
+    if (o.mode != kGivenLevel && o.mode != kGivenCells) return;  // uniform
+    const void* row = row_of<DT>(p, b);
+    const uint32_t groups = (uint32_t)((p.V + GN - 1) / GN), whole = (uint32_t)(p.V / GN);
+    u32x4 raw[kPartSteps];
+    const uint32_t g0 = load_part<DT, VEC>(row, part, groups, p.V, raw);
+    if (t < kOctave) root[t] = kRoot[t];
+    if (t == 0) {
+        list_n = sure_all = kmax_all = 0;
+        kmin_all = 0xFFFFFFFFu;
+    }
+    __syncthreads();
+    const int s_sure = o.mode == kGivenLevel || o.r_lo > o.top ? -1 : o.top - o.r_lo;
+    const int s_und = o.r_hi > o.top ? 0 : o.top - o.r_hi, s_bot = o.top - o.rb;
+    const bool apart = o.mode == kGivenCells && o.rb <= o.top && o.rb > o.r_hi;
+    for (int i = t; i <= kSlots; i += kPartThreads)
+        cell_mass[i] = i > s_sure && i <= o.top ? rank_weight(root, o.top - i) : 0.0;
+    __syncthreads();
+    const size_t at = (size_t)b * wk.C + part;
+    uint2* list = wk.list + at * kPartCap;
+    uint32_t sure_n = 0, und_n = 0, kmin = 0xFFFFFFFFu, kmax = 0;
+    double acc[2] = {0.0, 0.0};
+    const bool by_level = o.mode == kGivenLevel;
+    const float from = by_level ? o.c.lo : fmaxf(o.floor_x, o.c.lo);
+#pragma unroll
+    for (int i = 0; i < kPartSteps; ++i) {
+        const uint32_t g = g0 + i * kWave;
+        if (g < groups) {  // uniform
+            float x[GN], xc[GN];
+            tokens_of<DT>(raw[i], g + lane, g + kWave > whole, p.V, x);
+            float most = x[0];
+#pragma unroll
+            for (int j = 1; j < GN; ++j) most = fmaxf(most, x[j]);
+            if (lanes(most >= o.floor_x)) {  // uniform
+                uint64_t some[GN];
+                uint32_t n = 0;
+                double e[GN], q[GN], h[GN];
+                int sl[GN];
+                // (a token below floor_x falls into a slot of no mass below s_und,
+                // or by a level out of the window)
+#pragma unroll
+                for (int j = 0; j < GN; ++j)
+                    xc[j] = fmaxf(by_level ? (x[j] >= o.floor_x ? x[j] : from) : x[j], from);
+                slots_of<GN, true>(o.c, xc, sl, h);
+#pragma unroll
+                for (int j = 0; j < GN; ++j) e[j] = cell_mass[min((uint32_t)sl[j], (uint32_t)kSlots)];
+                in_cells(h, q);
+#pragma unroll
+                for (int j = 0; j < GN; ++j) {
+                    const uint64_t up = by_level ? lanes(x[j] >= o.floor_x) : lanes(sl[j] > s_sure);
+                    sure_n += (uint32_t)__builtin_popcountll(up);
+                    some[j] = by_level ? 0 : lanes(sl[j] >= s_und) & ~up;
+                    if (apart) some[j] |= lanes(sl[j] == s_bot);
+                    n += (uint32_t)__builtin_popcountll(some[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < GN; ++j) acc[j & 1] = fma(e[j], q[j], acc[j & 1]);
+                if (n) {  // uniform
+                    und_n += n;
+                    uint32_t next = 0;
+                    if (lane == 0) next = atomicAdd(&list_n, n);
+                    next = uniform(next);
+#pragma unroll
+                    for (int j = 0; j < GN; ++j) {
+                        if (some[j] >> lane & 1) {
+                            const uint32_t mine = next + __builtin_amdgcn_mbcnt_hi(
+                                (uint32_t)(some[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some[j], 0));
+                            const uint32_t key = order_key(x[j]);
+                            if (mine < kPartCap) list[mine] = make_uint2(__float_as_uint(x[j]), (g + lane) * GN + j);
+                            kmin = min(kmin, key);
+                            kmax = max(kmax, key);
+                        }
+                        next += (uint32_t)__builtin_popcountll(some[j]);
+                    }
+                }
+            }
+        }
+        if (i % kSubSteps == kSubSteps - 1) {
+            const double sum = wave_reduce(acc[0] + acc[1], SumF64());
+            const size_t seg = at * kPartSegs + w * (kPartSteps / kSubSteps) + i / kSubSteps;
+            if (lane == 0) {
+                wk.sub[seg] = sum;
+                wk.und[seg] = und_n;
+            }
+            acc[0] = acc[1] = 0.0;
+            und_n = 0;
+        }
+    }
+    if (lane == 0) atomicAdd(&sure_all, sure_n);
+    if (lanes(kmax != 0)) {  // uniform
+        kmin = wave_reduce(kmin, MinU32());
+        kmax = ~wave_reduce(~kmax, MinU32());
+        if (lane == 0) {
+            atomicMin(&kmin_all, kmin);
+            atomicMax(&kmax_all, kmax);
+        }
+    }
+    __syncthreads();
+    if (t == 0) wk.tail[at] = PartTail{list_n, sure_all, kmin_all, kmax_all};
+}
+
+template <int DT, bool VEC, int NT>
+__global__ __launch_bounds__(NT) void given_draw_kernel(GivenParams p, GivenWork wk)
+{
+    typedef GivenShared<NT> Shared;
+    constexpr int GN = Group<DT>::N;
+    __shared__ Shared sh;
+    __shared__ uint32_t s_at[kMaxParts], s_n[kMaxParts];
+    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+    const int64_t b = blockIdx.x;
+    RowState& st = wk.state[b];
+    const int mode = uniform(st.o.mode);
+    if (mode == kGivenAlone) {
+        whole_row<DT, VEC, NT>(sh, p, b);
+        return;
+    }
+    if (mode != kGivenLevel && mode != kGivenCells) {
+        store_single<NT>(p, b, uniform(st.token));
+        return;
+    }
+    const RowIn in = row_in(p, b);
+    const RowPlan o = st.o;
+    const void* row = row_of<DT>(p, b);
+    const uint32_t segs = (uint32_t)wk.C * kPartSegs;
+    Deal d;
+    d.groups = (uint32_t)((p.V + GN - 1) / GN);
+    d.steps = segs * kSubSteps;
+    d.sps = kSubSteps;
+    d.spw = segs;
+    if (t < kOctave) sh.root[t] = kRoot[t];
+    sh.sub[t] = t < (int)segs ? wk.sub[(size_t)b * segs + t] : 0.0;
+    sh.pre[t] = t < (int)segs ? (double)wk.und[(size_t)b * segs + t] : 0.0;
+    sh.subc[t] = 0;
+    uint32_t count = 0, kmin = 0xFFFFFFFFu, kmax = 0, n = 0;
+    if (t < wk.C) {
+        const PartTail tail = wk.tail[(size_t)b * wk.C + t];
+        count = tail.sure;
+        kmin = tail.kmin;
+        kmax = tail.kmax;
+        n = tail.listed;
+    }
+    uint32_t ln = 0;
+    bool listed = true;
+    if (o.mode == kGivenCells) {
+        // The parts' lists one after another; none where one does not fit.
+        const uint64_t before = block_exclusive_sum<NT>((uint64_t)n | (uint64_t)(n > kPartCap) << 40, sh.red64);
+        if (t < wk.C) {
+            s_at[t] = (uint32_t)before;
+            s_n[t] = n;
+        }
+        if (t == wk.C - 1) {
+            sh.n_window = (uint32_t)before + n;
+            sh.cross = (before >> 40) || n > kPartCap;
+        }
+        if (t == 0) {
+            sh.s_above = st.s_above;
+            sh.a_lo = st.a_lo;
+            sh.n_above = st.n_above;
+        }
+        const uint64_t* joined = wk.hist + (size_t)b * wk.C * kSlots;
+        for (int r = o.r_lo + t; r <= o.r_hi; r += NT) sh.hist[o.top - r] = joined[o.top - r];
+        if (t == 0 && o.rb <= o.top) sh.hist[o.top - o.rb] = joined[o.top - o.rb];
+        __syncthreads();
+        ln = uniform(sh.n_window);
+        listed = !uniform(sh.cross) && ln <= Shared::kCap;
+        if (listed) {
+            for (int i = w; i < wk.C; i += Shared::kWaves)
+                for (uint32_t k = lane; k < s_n[i]; k += kWave)
+                    sh.list[s_at[i] + k] = wk.list[((size_t)b * wk.C + i) * kPartCap + k];
+        } else {
+            for (uint32_t i = t; i < Shared::kCap; i += NT) sh.list[i].x = kEmpty;
+        }
+    }
+    __syncthreads();
+    double one_weight;
+    const Fixed fx(ldexp(1.0, p.bits));
+    const float low = resolve_row<DT, NT>(sh, p, row, d, in, o, fx, listed, ln, kmin, kmax, count, one_weight);
+    const double S = draw_row<DT, VEC, NT>(sh, p, b, row, d, segs, in, o, low, count, one_weight);
+    if (t == 0) {
+        st.S = S;
+        st.low = low;
+    }
+}
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kPartThreads) void given_probs_kernel(GivenParams p, GivenWork wk)
+{
+    constexpr int GN = Group<DT>::N;
+    __shared__ double root[kOctave];
+    const int t = threadIdx.x, lane = t & (kWave - 1);
+    const int64_t b = blockIdx.x / (uint32_t)wk.C;
+    const int part = (int)(blockIdx.x % (uint32_t)wk.C);
+    const RowState& st = wk.state[b];
+    const int mode = uniform(st.o.mode);
+    if (mode == kGivenAlone) return;  // written already
+    float* out = p.out_probs + b * p.V;
+    const bool vec = p.V % 4 == 0 && (uintptr_t)p.out_probs % 16 == 0;
+    const bool dist = mode == kGivenLevel || mode == kGivenCells;
+    const int token = dist ? -1 : uniform(st.token);
+    const uint32_t groups = (uint32_t)((p.V + GN - 1) / GN);
+    u32x4 raw[kPartSteps];
+    const uint32_t g0 = load_part<DT, VEC>(row_of<DT>(p, b), part, groups, p.V, raw);
+    if (t < kOctave) root[t] = kRoot[t];
+    __syncthreads();
+    const RowPlan o = st.o;
+    const float low = dist ? st.low : INFINITY;
+    const double inv = dist ? 1.0 / st.S : 0.0;
+#pragma unroll
+    for (int i = 0; i < kPartSteps; ++i) {
+        const uint32_t g = g0 + i * kWave + lane;
+        float x[GN], q[GN];
+        tokens_of<DT>(raw[i], g, true, p.V, x);
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < GN; ++j) {
+            q[j] = (int)(g * GN + j) == token ? 1.0f : 0.0f;
+            any |= x[j] >= low;
+        }
+        if (lanes(any)) {
+#pragma unroll
+            for (int j = 0; j < GN; ++j)
+                if (x[j] >= low) q[j] = (float)(weight_of(o, root, x[j]) * inv);
+        }
+        const int64_t i0 = (int64_t)g * GN;
+        if (vec && i0 + GN <= p.V) {
+#pragma unroll
+            for (int j = 0; j < GN; j += 4) *(f32x4*)(out + i0 + j) = f32x4{q[j], q[j + 1], q[j + 2], q[j + 3]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < GN; ++j)
+                if (i0 + j < p.V) out[i0 + j] = q[j];
+        }
     }
 }
 

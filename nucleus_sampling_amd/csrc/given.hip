@@ -19,20 +19,82 @@ bool other_options(const nucleus_options* o)
            o->split_give_up_row;
 }
 
-template <int DT>
-int launch_sample(const GivenParams& p, bool vec, hipStream_t s)
+// Rows are split where that is faster: ...
+int64_t parts_of(int64_t V, int32_t dtype)
 {
-    const dim3 grid((unsigned)p.B), block(512);
+    const int64_t tokens = dtype == NUCLEUS_F32 ? part_tokens<kF32>() : part_tokens<kBF16>();
+    const int64_t C = (V + tokens - 1) / tokens;
+    return C <= kMaxParts ? C : 0;
+}
+
+bool split_pays(int64_t B, int64_t V, int32_t dtype)
+{
+    const int64_t C = parts_of(V, dtype);
+    return C >= 3 && B < 512;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The workspace of a split batch, and its regions when `base` is given.
+size_t lay_out(int64_t B, int64_t C, char* base, GivenWork* wk)
+{
+    size_t at = 0;
+    const auto region = [&](size_t bytes) {
+        char* r = base + at;
+        at += align256(bytes);
+        return r;
+    };
+    const size_t parts = (size_t)B * (size_t)C;
+    GivenWork o;
+    o.state = (RowState*)region((size_t)B * sizeof(RowState));
+    o.head = (PartHead*)region(parts * sizeof(PartHead));
+    o.tail = (PartTail*)region(parts * sizeof(PartTail));
+    o.sub = (double*)region(parts * kPartSegs * 8);
+    o.und = (uint32_t*)region(parts * kPartSegs * 4);
+    o.list = (uint2*)region(parts * kPartCap * 8);
+    o.hist = (uint64_t*)region(parts * kSlots * 8);
+    o.cnt = (uint32_t*)region(parts * kSlots * 4);
+    o.C = (int)C;
+    if (wk) *wk = o;
+    return at;
+}
+
+template <int DT, bool VEC>
+void launch_rows(const GivenParams& p, const GivenWork* wk, hipStream_t s)
+{
+    const dim3 rows((unsigned)p.B), wide(kDrawThreads);
+    if (!wk) {
+        hipLaunchKernelGGL((given_row_kernel<DT, VEC, kDrawThreads>), rows, wide, 0, s, p);
+        return;
+    }
+    const dim3 parts((unsigned)(p.B * wk->C)), narrow(kPartThreads);
+    hipLaunchKernelGGL((given_hist_kernel<DT, VEC>), parts, narrow, 0, s, p, *wk);
+    hipLaunchKernelGGL((given_plan_kernel<kDrawThreads>), rows, wide, 0, s, p, *wk);
+    hipLaunchKernelGGL((given_mass_kernel<DT, VEC>), parts, narrow, 0, s, p, *wk);
+    hipLaunchKernelGGL((given_draw_kernel<DT, VEC, kDrawThreads>), rows, wide, 0, s, p, *wk);
+    if (p.out_probs) hipLaunchKernelGGL((given_probs_kernel<DT, VEC>), parts, narrow, 0, s, p, *wk);
+}
+
+template <int DT>
+int launch_sample(const GivenParams& p, bool vec, const GivenWork* wk, hipStream_t s)
+{
     if (vec)
-        hipLaunchKernelGGL((given_row_kernel<DT, true, 512>), grid, block, 0, s, p);
+        launch_rows<DT, true>(p, wk, s);
     else
-        hipLaunchKernelGGL((given_row_kernel<DT, false, 512>), grid, block, 0, s, p);
+        launch_rows<DT, false>(p, wk, s);
     return hipGetLastError() == hipSuccess ? NUCLEUS_OK : NUCLEUS_ELAUNCH;
 }
 
 size_t uniform_bytes(int32_t dtype) { return dtype == NUCLEUS_F64 ? 8 : 4; }
 
 }  // namespace
+
+extern "C" size_t nucleus_given_workspace_bytes(int64_t B, int64_t V, int32_t dtype)
+{
+    if (B < 1 || B >= (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31)) return 0;
+    if (dtype != NUCLEUS_F32 && dtype != NUCLEUS_BF16 && dtype != NUCLEUS_F16) return 0;
+    return split_pays(B, V, dtype) ? lay_out(B, parts_of(V, dtype), nullptr, nullptr) : 0;
+}
 
 extern "C" int nucleus_sample_given(const void* logits, int64_t B, int64_t V, const float* temperature,
                                     const float* top_p, const int32_t* top_k, const float* min_p, const void* uniforms,
@@ -54,6 +116,9 @@ extern "C" int nucleus_sample_given(const void* logits, int64_t B, int64_t V, co
         (uintptr_t)uniforms % uniform_bytes(uniform_dtype) || !aligned(out_token) || !aligned(out_keep_count) ||
         !aligned(out_token_logprob) || !aligned(out_probs))
         return NUCLEUS_EINVAL;
+    // Without a workspace every row runs on one workgroup.
+    const size_t need = o.workspace ? nucleus_given_workspace_bytes(B, V, o.dtype) : 0;
+    if (need && (o.workspace_bytes < need || (uintptr_t)o.workspace % 256)) return NUCLEUS_EWORKSPACE;
     const int dev_rc = check_device();
     if (dev_rc != NUCLEUS_OK) return dev_rc;
 
@@ -79,9 +144,12 @@ extern "C" int nucleus_sample_given(const void* logits, int64_t B, int64_t V, co
     while ((int64_t(1) << log2v) < V) ++log2v;
     p.bits = 62 - log2v < 50 ? 62 - log2v : 50;
     hipStream_t s = (hipStream_t)o.stream;
-    if (o.dtype == NUCLEUS_F32) return launch_sample<kF32>(p, vec, s);
-    if (o.dtype == NUCLEUS_BF16) return launch_sample<kBF16>(p, vec, s);
-    return launch_sample<kF16>(p, vec, s);
+    GivenWork wk;
+    if (need) lay_out(B, parts_of(V, o.dtype), (char*)o.workspace, &wk);
+    const GivenWork* split = need ? &wk : nullptr;
+    if (o.dtype == NUCLEUS_F32) return launch_sample<kF32>(p, vec, split, s);
+    if (o.dtype == NUCLEUS_BF16) return launch_sample<kBF16>(p, vec, split, s);
+    return launch_sample<kF16>(p, vec, split, s);
 }
 
 extern "C" size_t nucleus_spec_given_workspace_bytes(int64_t B, int64_t V)

@@ -75,6 +75,18 @@ def test_spec_given_workspace(L):
     assert L.nucleus_spec_given_workspace_bytes(-1, 8) == 0 and L.nucleus_spec_given_workspace_bytes(2, 0) == 0
 
 
+def test_sample_given_workspace(L):
+    """Long rows of smaller batches are split, if a workspace is given; one
+    that is too small or off its boundary is refused."""
+    size = L.nucleus_given_workspace_bytes
+    assert size(0, 128256, 0) == 0 and size(4, 0, 0) == 0 and size(4, 128256, 3) == 0
+    assert size(15, 1024, 0) == 0 and size(1, 128256, 0) > 0
+    assert size(4, 128256, 0) > size(1, 128256, 0)
+    need = size(2, 128256, 0)
+    assert _sample(L, V=128256, opt=_opt(workspace=1 << 40, workspace_bytes=need - 1)) == EWORKSPACE
+    assert _sample(L, V=128256, opt=_opt(workspace=(1 << 40) + 128, workspace_bytes=need)) == EWORKSPACE
+
+
 def test_the_other_entry_points_refuse_16_bit_floats(L):
     """NUCLEUS_F16 is the new calls' alone."""
     o = _opt(dtype=2)

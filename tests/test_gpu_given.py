@@ -89,24 +89,30 @@ def _check(x, T, p, k, mp, u, dtype="f32", what="", strict=True, pad=0, **kw):
     k = np.zeros(B, np.int32) if k is None else k
     mp = np.zeros(B, np.float32) if mp is None else mp
     say(f"sample_given {what} {dtype} B={B} V={x.shape[1]} N={u.shape[1]}")
-    got = ns.sample_given(lg, torch.from_numpy(T), torch.from_numpy(p), torch.from_numpy(u), torch.from_numpy(k),
-                          torch.from_numpy(mp), want_probs=True, **kw)
-    torch.cuda.synchronize()
     token, count, logprob, probs, near = _reference(x, T, p, k, mp, u)
     if strict:
         assert near > 1e-11, near
-    gt, gc = got.token.cpu().numpy(), got.keep_count.cpu().numpy()
-    assert np.array_equal(gc, count), (what, np.nonzero(gc != count)[0][:5], gc[gc != count][:5], count[gc != count][:5])
-    assert np.array_equal(gt, token), (what, np.argwhere(gt != token)[:5], gt[gt != token][:5], token[gt != token][:5])
-    # logprob: computed in double (errors ~1e-13 relative to the mass), rounded once.
-    gl = got.logprob.cpu().numpy().astype(np.float64)
-    ok = np.isnan(logprob)
-    assert np.array_equal(np.isnan(gl), ok)
-    assert (np.abs(gl - logprob)[~ok] <= 2.0**-24 * np.abs(logprob[~ok]) + 1e-11).all()
-    gp = got.probs.cpu().numpy().astype(np.float64)
-    # 2^-126: the smallest normal fp32; below it, its last place.
-    assert (np.abs(gp - probs) <= (2.0**-24 + 1e-11) * probs + 2.0**-149).all()
-    return got
+    results = []
+    for alone in (False, True):  # rows split over workgroups where that is the choice, and one workgroup a row
+        got = ns.sample_given(lg, torch.from_numpy(T), torch.from_numpy(p), torch.from_numpy(u), torch.from_numpy(k),
+                              torch.from_numpy(mp), want_probs=True, single_workgroup=alone, **kw)
+        torch.cuda.synchronize()
+        gt, gc = got.token.cpu().numpy(), got.keep_count.cpu().numpy()
+        say(what, "one workgroup a row" if alone else "default path")
+        assert np.array_equal(gc, count), (what, alone, np.nonzero(gc != count)[0][:5], gc[gc != count][:5],
+                                           count[gc != count][:5])
+        assert np.array_equal(gt, token), (what, alone, np.argwhere(gt != token)[:5], gt[gt != token][:5],
+                                           token[gt != token][:5])
+        # logprob: computed in double (errors ~1e-13 relative to the mass), rounded once.
+        gl = got.logprob.cpu().numpy().astype(np.float64)
+        ok = np.isnan(logprob)
+        assert np.array_equal(np.isnan(gl), ok)
+        assert (np.abs(gl - logprob)[~ok] <= 2.0**-24 * np.abs(logprob[~ok]) + 1e-11).all()
+        gp = got.probs.cpu().numpy().astype(np.float64)
+        # 2^-126: the smallest normal fp32; below it, its last place.
+        assert (np.abs(gp - probs) <= (2.0**-24 + 1e-11) * probs + 2.0**-149).all()
+        results.append(got)
+    return results[0]
 
 
 def _u(rng, B, N, dtype=np.float32):
@@ -129,7 +135,7 @@ def test_large_vocabulary_workloads(n, rows, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("V", [1, 2, 3, 7, 8, 9, 63, 257, 1000, 4097, 8192, 33001])
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 8, 9, 63, 257, 1000, 4097, 8192, 33001, 49152, 65537, 131073])
 def test_ragged_lengths(V, dtype):
     rng = np.random.default_rng(V)
     w = _random_batch(rng, 9, V, "f32")
