@@ -1022,27 +1022,15 @@ __device__ __forceinline__ double draw_row(Shared& sh, const GivenParams& p, int
     return S;
 }
 
-// One row on one workgroup.
+// The first pass over a row by one workgroup: its max, and where it wants
+// one the histogram in LDS (two copies) over lattice c.
 template <int DT, bool VEC, int NT, class Shared>
-__device__ __forceinline__ void whole_row(Shared& sh, const GivenParams& p, int64_t b)
+__device__ __forceinline__ void row_first_pass(Shared& sh, const GivenParams& p, const void* row, const Deal& d,
+                                               const RowIn& in, const Fixed& fx, Cells& c, FirstPass& f, float& m)
 {
     constexpr int GN = Group<DT>::N;
-    constexpr uint32_t kCap = Shared::kCap;
     const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
-    const void* row = row_of<DT>(p, b);
-    const Deal d = deal_out<DT, NT>(p.V);
-    const Fixed fx(ldexp(1.0, p.bits));
-    const RowIn in = row_in(p, b);
-
-    if (t < kOctave) sh.root[t] = kRoot[t];
-    sh.sub[t] = 0.0;
-    sh.pre[t] = 0.0;
-    sh.subc[t] = 0;
-    if (t == 0) sh.list_n = 0;
-
-    // ---- pass 1: max, NaN / +inf, histogram -----------------------------
-    Cells c = {};
-    FirstPass f;
+    c = Cells{};
     float anchor = -INFINITY;
     if (in.want_hist) {
         // The anchor: the max of every thread's first group.
@@ -1057,7 +1045,7 @@ __device__ __forceinline__ void whole_row(Shared& sh, const GivenParams& p, int6
         }
         anchor = uniform(block_reduce<NT>(anchor, MaxF32(), (float*)sh.redf));
     }
-    float m = -INFINITY;
+    m = -INFINITY;
     bool hist = in.want_hist && anchor > -INFINITY && anchor < INFINITY;
     // At most three turns: for the max alone where the first tokens were all
     // masked, with a histogram, and once more where the max lay above its window.
@@ -1090,23 +1078,52 @@ __device__ __forceinline__ void whole_row(Shared& sh, const GivenParams& p, int6
         }
         hist = true;
     }
+}
 
-    if (row_error(in, m) || in.greedy) {
-        int token = -1;
-        if (!row_error(in, m)) {
-            // The lowest index that holds the max: every thread knows the step
-            // that first held its own.
-            uint32_t first = 0xFFFFFFFFu;
-            if (f.m == m) {
-                const uint32_t g = ((uint32_t)w * d.steps + f.at) * kWave + lane;
-                float x[GN];
-                tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
+// The token of a greedy row: the lowest index that holds the max.  Every
+// thread knows the step that first held its own.
+template <int DT, bool VEC, int NT, class Shared>
+__device__ __forceinline__ int greedy_token(Shared& sh, const GivenParams& p, const void* row, const Deal& d,
+                                            const FirstPass& f, float m)
+{
+    constexpr int GN = Group<DT>::N;
+    const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+    uint32_t first = 0xFFFFFFFFu;
+    if (f.m == m) {
+        const uint32_t g = ((uint32_t)w * d.steps + f.at) * kWave + lane;
+        float x[GN];
+        tokens_of<DT>(load_raw<DT, VEC>(row, g, d.groups, p.V), g, true, p.V, x);
 #pragma unroll
-                for (int j = GN - 1; j >= 0; --j)
-                    if (x[j] == m) first = g * GN + j;
-            }
-            token = (int)block_reduce<NT>(first, MinU32(), (uint32_t*)sh.red64);
-        }
+        for (int j = GN - 1; j >= 0; --j)
+            if (x[j] == m) first = g * GN + j;
+    }
+    return (int)block_reduce<NT>(first, MinU32(), (uint32_t*)sh.red64);
+}
+
+// One row on one workgroup.
+template <int DT, bool VEC, int NT, class Shared>
+__device__ __forceinline__ void whole_row(Shared& sh, const GivenParams& p, int64_t b)
+{
+    constexpr int GN = Group<DT>::N;
+    constexpr uint32_t kCap = Shared::kCap;
+    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+    const void* row = row_of<DT>(p, b);
+    const Deal d = deal_out<DT, NT>(p.V);
+    const Fixed fx(ldexp(1.0, p.bits));
+    const RowIn in = row_in(p, b);
+
+    if (t < kOctave) sh.root[t] = kRoot[t];
+    sh.sub[t] = 0.0;
+    sh.pre[t] = 0.0;
+    sh.subc[t] = 0;
+    if (t == 0) sh.list_n = 0;
+
+    Cells c;
+    FirstPass f;
+    float m;
+    row_first_pass<DT, VEC, NT>(sh, p, row, d, in, fx, c, f, m);
+    if (row_error(in, m) || in.greedy) {
+        const int token = row_error(in, m) ? -1 : greedy_token<DT, VEC, NT>(sh, p, row, d, f, m);
         store_single<NT>(p, b, token);
         if (p.out_probs)
             for (int64_t i = t; i < p.V; i += NT) p.out_probs[b * p.V + i] = i == token ? 1.0f : 0.0f;
@@ -1306,8 +1323,11 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
 
 // ---------------------------------------------------------------------------
 // Rows split over workgroups.  A part is 32 KB of a row, held in the registers
-// of one 256-thread workgroup; four launches (five with the distribution):
+// of one 256-thread workgroup; three or four launches (one more with the
+// distribution):
 //
+//   given_first_kernel  per row: first pass and cells of the cuts, where there
+//                       are rows enough to fill the device; else
 //   given_hist_kernel   per part: max and histogram, over a lattice anchored
 //                       at the max of 256 groups spread over the whole row
 //                       (every part of a row reads the same ones)
@@ -1330,6 +1350,7 @@ constexpr int kPartSegs = kPartWaves * kPartSteps / kSubSteps;       // segments
 constexpr int kPartCap = 1024;                                       // listed tokens
 constexpr int kMaxParts = 64;                                        // of a row: its segments fit one per thread
 constexpr int kDrawThreads = 512;
+constexpr int kMassCells = 2304;                                     // kept cells of a split row, at most
 static_assert(kMaxParts * kPartSegs <= kDrawThreads, "one segment per thread of given_draw_kernel");
 
 template <int DT>
@@ -1357,8 +1378,9 @@ struct GivenWork {
     RowState* state;   // [B]
     PartHead* head;    // [B][C]
     PartTail* tail;    // [B][C]
-    uint64_t* hist;    // [B][C][kSlots]; part 0's holds the joined cells of the cuts after given_plan_kernel
-    uint32_t* cnt;     // [B][C][kSlots]
+    uint64_t* joined;  // [B][kSlots]: the histogram at the cells of the cuts
+    uint64_t* hist;    // [B][C][kSlots] (given_hist_kernel)
+    uint32_t* cnt;     // [B][C][kSlots] (given_hist_kernel)
     double* sub;       // [B][C][kPartSegs]
     uint32_t* und;     // [B][C][kPartSegs]
     uint2* list;       // [B][C][kPartCap]
@@ -1487,6 +1509,28 @@ __global__ __launch_bounds__(kPartThreads) void given_hist_kernel(GivenParams p,
     if (t == 0) wk.head[b * wk.C + part] = o;
 }
 
+// A planned row's state for the kernels that follow.
+template <int NT, class Shared>
+__device__ __forceinline__ void hand_on(Shared& sh, const GivenWork& wk, int64_t b, RowPlan o)
+{
+    const int t = threadIdx.x;
+    const int kept = o.mode == kGivenLevel || o.r_lo > o.top ? o.top + 1 : o.r_lo;  // cells
+    if (!o.c.fast || (o.mode == kGivenCells && o.rb == o.top + 1) || kept > kMassCells) o.mode = kGivenAlone;
+    __syncthreads();
+    if (o.mode == kGivenCells) {
+        uint64_t* joined = wk.joined + (size_t)b * kSlots;
+        for (int r = o.r_lo + t; r <= o.r_hi; r += NT) joined[o.top - r] = sh.hist[o.top - r];
+        if (t == 0 && o.rb <= o.top) joined[o.top - o.rb] = sh.hist[o.top - o.rb];
+    }
+    if (t == 0) {
+        RowState& st = wk.state[b];
+        st.o = o;
+        st.s_above = sh.s_above;
+        st.a_lo = sh.a_lo;
+        st.n_above = sh.n_above;
+    }
+}
+
 template <int NT>
 __global__ __launch_bounds__(NT) void given_plan_kernel(GivenParams p, GivenWork wk)
 {
@@ -1527,20 +1571,38 @@ __global__ __launch_bounds__(NT) void given_plan_kernel(GivenParams p, GivenWork
         }
         if (!alone) {
             if (in.use_k) finite = (uint32_t)block_reduce<NT>((uint64_t)mine.finite, SumU64(), sh.red64);
+            // Eight slots a thread, all parts' words of them in flight together; a
+            // slot outside a part's range reads the range's end and drops it.
+            constexpr int PER = kSlots / NT;
             const uint64_t* hist = wk.hist + (size_t)b * wk.C * kSlots;
             const uint32_t* cnt = wk.cnt + (size_t)b * wk.C * kSlots;
-            for (int sl = t; sl < kSlots; sl += NT) {
-                uint64_t h = 0;
-                uint32_t n = 0;
-#pragma unroll 8
-                for (int i = 0; i < wk.C; ++i)
-                    if (sl >= s_lo[i] && sl <= s_hi[i]) h += hist[(size_t)i * kSlots + sl];
-                if (in.use_k)
-#pragma unroll 8
-                    for (int i = 0; i < wk.C; ++i)
-                        if (sl >= s_lo[i] && sl <= s_hi[i]) n += cnt[(size_t)i * kSlots + sl];
-                sh.hist[sl] = h;
-                sh.cnt[sl] = n;
+            uint64_t h[PER] = {};
+            uint32_t n[PER] = {};
+#pragma unroll 4
+            for (int i = 0; i < wk.C; ++i) {
+                const int lo = s_lo[i], hi = s_hi[i];
+                if (lo > hi) continue;  // uniform: a part without a token in the window
+                uint64_t v[PER];
+#pragma unroll
+                for (int k = 0; k < PER; ++k) v[k] = hist[(size_t)i * kSlots + min(max(t + k * NT, lo), hi)];
+#pragma unroll
+                for (int k = 0; k < PER; ++k) h[k] += t + k * NT >= lo && t + k * NT <= hi ? v[k] : 0;
+            }
+            if (in.use_k)
+#pragma unroll 4
+                for (int i = 0; i < wk.C; ++i) {
+                    const int lo = s_lo[i], hi = s_hi[i];
+                    if (lo > hi) continue;  // uniform
+                    uint32_t v[PER];
+#pragma unroll
+                    for (int k = 0; k < PER; ++k) v[k] = cnt[(size_t)i * kSlots + min(max(t + k * NT, lo), hi)];
+#pragma unroll
+                    for (int k = 0; k < PER; ++k) n[k] += t + k * NT >= lo && t + k * NT <= hi ? v[k] : 0;
+                }
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                sh.hist[t + k * NT] = h[k];
+                sh.cnt[t + k * NT] = n[k];
             }
         }
     }
@@ -1549,27 +1611,42 @@ __global__ __launch_bounds__(NT) void given_plan_kernel(GivenParams p, GivenWork
         if (t == 0) st.o.mode = kGivenAlone;
         return;
     }
-    RowPlan o = plan_row<NT>(sh, in, c, m, finite, false, p.bits);
-    if (!o.c.fast || (o.mode == kGivenCells && o.rb == o.top + 1)) o.mode = kGivenAlone;
-    __syncthreads();
-    if (o.mode == kGivenCells) {
-        uint64_t* joined = wk.hist + (size_t)b * wk.C * kSlots;
-        for (int r = o.r_lo + t; r <= o.r_hi; r += NT) joined[o.top - r] = sh.hist[o.top - r];
-        if (t == 0 && o.rb <= o.top) joined[o.top - o.rb] = sh.hist[o.top - o.rb];
+    hand_on<NT>(sh, wk, b, plan_row<NT>(sh, in, c, m, finite, false, p.bits));
+}
+
+template <int DT, bool VEC, int NT>
+__global__ __launch_bounds__(NT) void given_first_kernel(GivenParams p, GivenWork wk)
+{
+    __shared__ GivenShared<NT> sh;
+    const int t = threadIdx.x, lane = t & (kWave - 1);
+    const int64_t b = blockIdx.x;
+    const void* row = row_of<DT>(p, b);
+    const Deal d = deal_out<DT, NT>(p.V);
+    const Fixed fx(ldexp(1.0, p.bits));
+    const RowIn in = row_in(p, b);
+    if (t < kOctave) sh.root[t] = kRoot[t];
+    Cells c;
+    FirstPass f;
+    float m;
+    row_first_pass<DT, VEC, NT>(sh, p, row, d, in, fx, c, f, m);
+    if (row_error(in, m) || in.greedy) {
+        const int token = row_error(in, m) ? -1 : greedy_token<DT, VEC, NT>(sh, p, row, d, f, m);
+        if (t == 0) {
+            wk.state[b].o.mode = token < 0 ? kGivenError : kGivenGreedy;
+            wk.state[b].token = token;
+        }
+        return;
     }
-    if (t == 0) {
-        st.o = o;
-        st.s_above = sh.s_above;
-        st.a_lo = sh.a_lo;
-        st.n_above = sh.n_above;
-    }
+    uint32_t finite = 0;
+    if (in.use_k) finite = (uint32_t)block_reduce<NT>((uint64_t)(lane == 0 ? f.finite : 0), SumU64(), sh.red64);
+    hand_on<NT>(sh, wk, b, plan_row<NT>(sh, in, c, m, finite, true, p.bits));
 }
 
 template <int DT, bool VEC>
 __global__ __launch_bounds__(kPartThreads) void given_mass_kernel(GivenParams p, GivenWork wk)
 {
     constexpr int GN = Group<DT>::N;
-    __shared__ double cell_mass[kSlots + 1];
+    __shared__ double cell_mass[kMassCells + 1];
     __shared__ double root[kOctave];
     __shared__ uint32_t list_n, sure_all, kmin_all, kmax_all;
     const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
@@ -1590,8 +1667,10 @@ __global__ __launch_bounds__(kPartThreads) void given_mass_kernel(GivenParams p,
     const int s_sure = o.mode == kGivenLevel || o.r_lo > o.top ? -1 : o.top - o.r_lo;
     const int s_und = o.r_hi > o.top ? 0 : o.top - o.r_hi, s_bot = o.top - o.rb;
     const bool apart = o.mode == kGivenCells && o.rb <= o.top && o.rb > o.r_hi;
-    for (int i = t; i <= kSlots; i += kPartThreads)
-        cell_mass[i] = i > s_sure && i <= o.top ? rank_weight(root, o.top - i) : 0.0;
+    // Masses of the surely kept cells from slot s_sure + 1 up, and 0 for every other.
+    const uint32_t cells = (uint32_t)(o.top - s_sure);
+    for (uint32_t i = t; i < cells; i += kPartThreads) cell_mass[i] = rank_weight(root, o.top - s_sure - 1 - (int)i);
+    if (t == 0) cell_mass[cells] = 0.0;
     __syncthreads();
     const size_t at = (size_t)b * wk.C + part;
     uint2* list = wk.list + at * kPartCap;
@@ -1620,7 +1699,7 @@ __global__ __launch_bounds__(kPartThreads) void given_mass_kernel(GivenParams p,
                     xc[j] = fmaxf(by_level ? (x[j] >= o.floor_x ? x[j] : from) : x[j], from);
                 slots_of<GN, true>(o.c, xc, sl, h);
 #pragma unroll
-                for (int j = 0; j < GN; ++j) e[j] = cell_mass[min((uint32_t)sl[j], (uint32_t)kSlots)];
+                for (int j = 0; j < GN; ++j) e[j] = cell_mass[min((uint32_t)(sl[j] - s_sure - 1), cells)];
                 in_cells(h, q);
 #pragma unroll
                 for (int j = 0; j < GN; ++j) {
@@ -1686,36 +1765,41 @@ __global__ __launch_bounds__(NT) void given_draw_kernel(GivenParams p, GivenWork
     const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
     const int64_t b = blockIdx.x;
     RowState& st = wk.state[b];
-    const int mode = uniform(st.o.mode);
+    const uint32_t segs = (uint32_t)wk.C * kPartSegs;
+    // Everything that does not depend on the row's mode is asked for at once
+    // (each wait for memory that other workgroups wrote costs about 1 us).
+    const RowState s0 = st;
+    double sub = 0.0;
+    uint32_t und = 0;
+    PartTail tail = {0, 0, 0xFFFFFFFFu, 0};
+    if (t < (int)segs) {
+        sub = wk.sub[(size_t)b * segs + t];
+        und = wk.und[(size_t)b * segs + t];
+    }
+    if (t < wk.C) tail = wk.tail[(size_t)b * wk.C + t];
+    const RowIn in = row_in(p, b);
+    const int mode = uniform(s0.o.mode);
     if (mode == kGivenAlone) {
         whole_row<DT, VEC, NT>(sh, p, b);
         return;
     }
     if (mode != kGivenLevel && mode != kGivenCells) {
-        store_single<NT>(p, b, uniform(st.token));
+        store_single<NT>(p, b, uniform(s0.token));
         return;
     }
-    const RowIn in = row_in(p, b);
-    const RowPlan o = st.o;
+    const RowPlan o = s0.o;
     const void* row = row_of<DT>(p, b);
-    const uint32_t segs = (uint32_t)wk.C * kPartSegs;
     Deal d;
     d.groups = (uint32_t)((p.V + GN - 1) / GN);
     d.steps = segs * kSubSteps;
     d.sps = kSubSteps;
     d.spw = segs;
     if (t < kOctave) sh.root[t] = kRoot[t];
-    sh.sub[t] = t < (int)segs ? wk.sub[(size_t)b * segs + t] : 0.0;
-    sh.pre[t] = t < (int)segs ? (double)wk.und[(size_t)b * segs + t] : 0.0;
+    sh.sub[t] = sub;
+    sh.pre[t] = (double)und;
     sh.subc[t] = 0;
-    uint32_t count = 0, kmin = 0xFFFFFFFFu, kmax = 0, n = 0;
-    if (t < wk.C) {
-        const PartTail tail = wk.tail[(size_t)b * wk.C + t];
-        count = tail.sure;
-        kmin = tail.kmin;
-        kmax = tail.kmax;
-        n = tail.listed;
-    }
+    uint32_t count = tail.sure, kmin = tail.kmin, kmax = tail.kmax;
+    const uint32_t n = tail.listed;
     uint32_t ln = 0;
     bool listed = true;
     if (o.mode == kGivenCells) {
@@ -1730,20 +1814,28 @@ __global__ __launch_bounds__(NT) void given_draw_kernel(GivenParams p, GivenWork
             sh.cross = (before >> 40) || n > kPartCap;
         }
         if (t == 0) {
-            sh.s_above = st.s_above;
-            sh.a_lo = st.a_lo;
-            sh.n_above = st.n_above;
+            sh.s_above = s0.s_above;
+            sh.a_lo = s0.a_lo;
+            sh.n_above = s0.n_above;
         }
-        const uint64_t* joined = wk.hist + (size_t)b * wk.C * kSlots;
+        const uint64_t* joined = wk.joined + (size_t)b * kSlots;
         for (int r = o.r_lo + t; r <= o.r_hi; r += NT) sh.hist[o.top - r] = joined[o.top - r];
         if (t == 0 && o.rb <= o.top) sh.hist[o.top - o.rb] = joined[o.top - o.rb];
         __syncthreads();
         ln = uniform(sh.n_window);
         listed = !uniform(sh.cross) && ln <= Shared::kCap;
         if (listed) {
-            for (int i = w; i < wk.C; i += Shared::kWaves)
-                for (uint32_t k = lane; k < s_n[i]; k += kWave)
-                    sh.list[s_at[i] + k] = wk.list[((size_t)b * wk.C + i) * kPartCap + k];
+            for (int i = w; i < wk.C; i += Shared::kWaves) {
+                const uint2* from = wk.list + ((size_t)b * wk.C + i) * kPartCap;
+                for (uint32_t k = lane; k < s_n[i]; k += 4 * kWave) {
+                    uint2 e[4];  // (places past the part's last are read, and left)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e[j] = from[min(k + j * kWave, (uint32_t)kPartCap - 1)];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (k + j * kWave < s_n[i]) sh.list[s_at[i] + k + j * kWave] = e[j];
+                }
+            }
         } else {
             for (uint32_t i = t; i < Shared::kCap; i += NT) sh.list[i].x = kEmpty;
         }

@@ -27,6 +27,8 @@ int64_t parts_of(int64_t V, int32_t dtype)
     return C <= kMaxParts ? C : 0;
 }
 
+constexpr int64_t kRowsFirst = 64;
+
 bool split_pays(int64_t B, int64_t V, int32_t dtype)
 {
     const int64_t C = parts_of(V, dtype);
@@ -52,8 +54,13 @@ size_t lay_out(int64_t B, int64_t C, char* base, GivenWork* wk)
     o.sub = (double*)region(parts * kPartSegs * 8);
     o.und = (uint32_t*)region(parts * kPartSegs * 4);
     o.list = (uint2*)region(parts * kPartCap * 8);
-    o.hist = (uint64_t*)region(parts * kSlots * 8);
-    o.cnt = (uint32_t*)region(parts * kSlots * 4);
+    o.joined = (uint64_t*)region((size_t)B * kSlots * 8);
+    o.hist = nullptr;
+    o.cnt = nullptr;
+    if (B < kRowsFirst) {
+        o.hist = (uint64_t*)region(parts * kSlots * 8);
+        o.cnt = (uint32_t*)region(parts * kSlots * 4);
+    }
     o.C = (int)C;
     if (wk) *wk = o;
     return at;
@@ -68,8 +75,12 @@ void launch_rows(const GivenParams& p, const GivenWork* wk, hipStream_t s)
         return;
     }
     const dim3 parts((unsigned)(p.B * wk->C)), narrow(kPartThreads);
-    hipLaunchKernelGGL((given_hist_kernel<DT, VEC>), parts, narrow, 0, s, p, *wk);
-    hipLaunchKernelGGL((given_plan_kernel<kDrawThreads>), rows, wide, 0, s, p, *wk);
+    if (wk->hist) {
+        hipLaunchKernelGGL((given_hist_kernel<DT, VEC>), parts, narrow, 0, s, p, *wk);
+        hipLaunchKernelGGL((given_plan_kernel<kDrawThreads>), rows, wide, 0, s, p, *wk);
+    } else {
+        hipLaunchKernelGGL((given_first_kernel<DT, VEC, kDrawThreads>), rows, wide, 0, s, p, *wk);
+    }
     hipLaunchKernelGGL((given_mass_kernel<DT, VEC>), parts, narrow, 0, s, p, *wk);
     hipLaunchKernelGGL((given_draw_kernel<DT, VEC, kDrawThreads>), rows, wide, 0, s, p, *wk);
     if (p.out_probs) hipLaunchKernelGGL((given_probs_kernel<DT, VEC>), parts, narrow, 0, s, p, *wk);
