@@ -1872,7 +1872,7 @@ __global__ __launch_bounds__(kPartThreads) void given_probs_kernel(GivenParams p
     if (t < kOctave) root[t] = kRoot[t];
     __syncthreads();
     const RowPlan o = st.o;
-    const float low = dist ? st.low : INFINITY;
+    const float low = dist ? st.low : NAN;  // (no logit is at or above it, +inf neither)
     const double inv = dist ? 1.0 / st.S : 0.0;
 #pragma unroll
     for (int i = 0; i < kPartSteps; ++i) {

@@ -19,7 +19,6 @@ bool other_options(const nucleus_options* o)
            o->split_give_up_row;
 }
 
-// Rows are split where that is faster: ...
 int64_t parts_of(int64_t V, int32_t dtype)
 {
     const int64_t tokens = dtype == NUCLEUS_F32 ? part_tokens<kF32>() : part_tokens<kBF16>();
@@ -27,13 +26,27 @@ int64_t parts_of(int64_t V, int32_t dtype)
     return C <= kMaxParts ? C : 0;
 }
 
-constexpr int64_t kRowsFirst = 64;
-
+// Rows are split where that is faster.  Up to 128 rows leave CUs idle at one
+// workgroup a row, but the split's launches cost 10 to 20 us whatever the row:
+// it pays from 40960 float32 and 49152 16-bit logits a row (us split / on one
+// workgroup, float32: 1 row of 32768 35 / 31, of 65536 38 / 46, of 128256
+// 42 / 73; 128 rows of 65536 49 / 51, of 128256 66 / 80; bf16: 8 rows of 32768
+// 42 / 35, of 65536 46 / 48, of 128256 50 / 76; 128 rows of 128256 68 / 80).
+// With more rows one workgroup a row fills the device (256 rows of 65536
+// float32 61 / 57, of 128256 bf16 87 / 81).  Float32 rows of 12 parts and more
+// are split at any batch: 256 alike rows of 128256 84 / 85 and 1024 302 / 321,
+// and where the rows' kept sets differ in size one workgroup waits for the
+// largest (84 / 97).
 bool split_pays(int64_t B, int64_t V, int32_t dtype)
 {
     const int64_t C = parts_of(V, dtype);
-    return C >= 3 && B < 512;
+    return (C >= (dtype == NUCLEUS_F32 ? 6 : 4) && B <= 128) || (C >= 12 && dtype == NUCLEUS_F32);
 }
+
+// Up to this many rows the first pass is split too; from there one workgroup
+// a row is faster (rows of 128256 float32: 1 row 42 / 45 us, 32 rows 52 / 52,
+// 64 rows 62 / 57).
+constexpr int64_t kSplitFirst = 32;
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -57,7 +70,7 @@ size_t lay_out(int64_t B, int64_t C, char* base, GivenWork* wk)
     o.joined = (uint64_t*)region((size_t)B * kSlots * 8);
     o.hist = nullptr;
     o.cnt = nullptr;
-    if (B < kRowsFirst) {
+    if (B <= kSplitFirst) {
         o.hist = (uint64_t*)region(parts * kSlots * 8);
         o.cnt = (uint32_t*)region(parts * kSlots * 4);
     }

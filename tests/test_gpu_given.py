@@ -234,6 +234,34 @@ def test_max_above_the_window():
     _check(x, T, p, k, None, _u(rng, 4, 4), what="max above the window")
 
 
+@pytest.mark.parametrize("dtype,V", [("f32", 45001), ("bf16", 50000)])
+@pytest.mark.parametrize("B", [3, 36])
+def test_every_kind_of_row_in_a_split_batch(B, dtype, V):
+    """Few and many long rows: planned from parts, or by one workgroup each."""
+    rng = np.random.default_rng(B * V)
+    x = rng.normal(0, 2, (36, V)).astype(np.float32)
+    T, p = rng.uniform(0.5, 1.5, 36).astype(np.float32), rng.uniform(0.3, 1.0, 36).astype(np.float32)
+    k, mp = np.zeros(36, np.int32), np.zeros(36, np.float32)
+    x[0] = np.linspace(0, 0.02, V)[rng.permutation(V)]   # more undecided tokens than a part lists
+    x[1] = rng.normal(-400, 2, V)
+    x[1, V - 2] = 300.0                                    # the max above the window
+    x[2], k[2], T[2] = rng.normal(0, 3, V), V // 2, 0.02   # the k-th token below the window
+    x[3], T[3] = -np.inf, 1.0
+    x[3, [5, 44000]] = [1.0, 2.0]                          # two tokens left
+    x[4] = np.nan                                          # errors
+    x[5, 17] = np.inf
+    x[6] = -np.inf
+    T[7] = 0.0                                             # greedy
+    k[8], k[9], k[10] = 1, 50, V + 7
+    p[11], p[12], mp[12] = 1.0, 1.0, 0.1
+    x[13] = 1.5                                            # all tied
+    x[14, V // 2:] = np.finfo(np.float32).min if dtype == "f32" else -1e38
+    x = x[rng.permutation(36)[:B]] if B < 36 else x
+    td = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    x = torch.from_numpy(x).to(td).float().numpy()
+    _check(x, T[:B], p[:B], k[:B], mp[:B], _u(rng, B, 3), dtype, what="split batch", strict=False)
+
+
 def test_rows_of_two_million_tokens():
     rng = np.random.default_rng(7)
     x = rng.normal(0, 2, (2, (1 << 21) + 5)).astype(np.float32)
