@@ -373,8 +373,8 @@ struct GivenShared {
     // a few percent of the row are common).  In the second pass the second
     // copy's place holds the weights 2^(-rank/32) of the surely kept cells, as
     // doubles, and 0 elsewhere.
-    uint64_t hist[2 * kCopy];
-    uint32_t cnt[kSlots + kWave];
+    alignas(16) uint64_t hist[2 * kCopy];
+    alignas(16) uint32_t cnt[kSlots + kWave];
     uint2 list[kCap];          // logit, index
     double sub[NT];            // mass of each segment's surely kept tokens; then of the segments up to it (-1: empty)
     uint64_t subc[NT];         // mass of its kept listed tokens, at 2^-bits
@@ -1531,6 +1531,45 @@ __device__ __forceinline__ void hand_on(Shared& sh, const GivenWork& wk, int64_t
     }
 }
 
+typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// The sums over the parts of their slots lo[i] .. hi[i], to LDS.
+template <int NT, class Pair, class Word>
+__device__ __forceinline__ void merge_parts(const Word* parts, const int* lo, const int* hi, int C, Word* out)
+{
+    constexpr int PER = kSlots / (2 * NT), AT_ONCE = 8;
+    const int t = threadIdx.x;
+    Pair sum[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) sum[k] = Pair{0, 0};
+#pragma unroll 1
+    for (int i0 = 0; i0 < C; i0 += AT_ONCE) {
+        Pair v[AT_ONCE][PER];
+        int a[AT_ONCE], e[AT_ONCE];
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j) {
+            const int i = min(i0 + j, C - 1);
+            a[j] = uniform(lo[i]);
+            e[j] = uniform(hi[i]);
+            const Pair* from = (const Pair*)(parts + (size_t)i * kSlots);
+#pragma unroll
+            for (int k = 0; k < PER; ++k) v[j][k] = from[min(max(t + k * NT, min(a[j], e[j]) >> 1), max(e[j], 0) >> 1)];
+            if (i0 + j >= C) e[j] = -1;
+        }
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j)
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int sl = 2 * (t + k * NT);
+                sum[k].x += sl >= a[j] && sl <= e[j] ? v[j][k].x : 0;
+                sum[k].y += sl + 1 >= a[j] && sl + 1 <= e[j] ? v[j][k].y : 0;
+            }
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) ((Pair*)out)[t + k * NT] = sum[k];
+}
+
 template <int NT>
 __global__ __launch_bounds__(NT) void given_plan_kernel(GivenParams p, GivenWork wk)
 {
@@ -1571,39 +1610,12 @@ __global__ __launch_bounds__(NT) void given_plan_kernel(GivenParams p, GivenWork
         }
         if (!alone) {
             if (in.use_k) finite = (uint32_t)block_reduce<NT>((uint64_t)mine.finite, SumU64(), sh.red64);
-            // Eight slots a thread, all parts' words of them in flight together; a
-            // slot outside a part's range reads the range's end and drops it.
-            constexpr int PER = kSlots / NT;
-            const uint64_t* hist = wk.hist + (size_t)b * wk.C * kSlots;
-            const uint32_t* cnt = wk.cnt + (size_t)b * wk.C * kSlots;
-            uint64_t h[PER] = {};
-            uint32_t n[PER] = {};
-#pragma unroll 4
-            for (int i = 0; i < wk.C; ++i) {
-                const int lo = s_lo[i], hi = s_hi[i];
-                if (lo > hi) continue;  // uniform: a part without a token in the window
-                uint64_t v[PER];
-#pragma unroll
-                for (int k = 0; k < PER; ++k) v[k] = hist[(size_t)i * kSlots + min(max(t + k * NT, lo), hi)];
-#pragma unroll
-                for (int k = 0; k < PER; ++k) h[k] += t + k * NT >= lo && t + k * NT <= hi ? v[k] : 0;
-            }
-            if (in.use_k)
-#pragma unroll 4
-                for (int i = 0; i < wk.C; ++i) {
-                    const int lo = s_lo[i], hi = s_hi[i];
-                    if (lo > hi) continue;  // uniform
-                    uint32_t v[PER];
-#pragma unroll
-                    for (int k = 0; k < PER; ++k) v[k] = cnt[(size_t)i * kSlots + min(max(t + k * NT, lo), hi)];
-#pragma unroll
-                    for (int k = 0; k < PER; ++k) n[k] += t + k * NT >= lo && t + k * NT <= hi ? v[k] : 0;
-                }
-#pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                sh.hist[t + k * NT] = h[k];
-                sh.cnt[t + k * NT] = n[k];
-            }
+            // Four pairs of slots a thread, eight parts' words of them in flight
+            // together: what other workgroups wrote takes 1 to 2 us to arrive,
+            // however many loads wait for it (16 parts: two at a time 8 us, eight 5).  A
+            // pair outside a part's range reads the range's end and drops it.
+            merge_parts<NT, u64x2>(wk.hist + (size_t)b * wk.C * kSlots, s_lo, s_hi, wk.C, sh.hist);
+            if (in.use_k) merge_parts<NT, u32x2>(wk.cnt + (size_t)b * wk.C * kSlots, s_lo, s_hi, wk.C, sh.cnt);
         }
     }
     __syncthreads();
