@@ -601,6 +601,34 @@ def _sample_given(handle, dev, logits, temperature, top_p, uniforms, top_k, min_
     return res
 
 
+def sample_hidden(hidden: torch.Tensor, weight: torch.Tensor, temperature, top_p, top_k=None, min_p=None, *,
+                  uniforms=None, bias: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                  logits: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None, **how):
+    """Sample from a model's last hidden states: ``project`` makes the float32
+    logits ``hidden @ weight.T + bias`` (soft-capped with ``softcap`` > 0), and
+    ``sample_given`` draws from them with ``uniforms``, or without any
+    ``sample`` does.
+
+    ``hidden`` is [B, K], ``weight`` [V, K].  ``logits`` may supply the [B, V]
+    tensor of the logits (float32, or where the sampler takes it the inputs'
+    type).  ``how``: the further keyword arguments of ``sample_given`` or
+    ``sample`` (``want_probs``, ``out``; ``seed``, ``step``, ``history``, ...).
+    Launches on ``stream`` (default: the current stream) and returns without
+    synchronising."""
+    how = dict(how, top_k=top_k, min_p=min_p)
+    if uniforms is not None:
+        call, args = sample_given, (temperature, top_p, uniforms)
+    else:
+        call, args = sample, (temperature, top_p)
+
+    def run(_):
+        made = project(hidden, weight, bias, activation="softcap" if softcap else "none", softcap=softcap,
+                       out_dtype=None if logits is not None else torch.float32, out=logits)
+        return call(made, *args, **how)
+
+    return _on(_on_gpu(hidden, "hidden"), stream, run)
+
+
 def spec_verify_given(target_probs: torch.Tensor, draft_probs: torch.Tensor, draft_token, uniforms, *,
                       out: Optional[SpecResult] = None, stream: Optional[torch.cuda.Stream] = None) -> SpecResult:
     """``spec_verify`` from ``uniforms`` [B, 2] that the caller brings

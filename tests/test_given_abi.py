@@ -109,3 +109,12 @@ def test_binding_refuses_what_it_cannot_take():
         ns.sample_given(x.requires_grad_(), 1.0, 0.9, u)
     with pytest.raises(ValueError):
         ns.spec_verify_given(torch.zeros(2, 8), torch.zeros(2, 8), [0, 0], torch.zeros(2, 2))
+
+
+def test_sample_hidden_has_no_cpu_path():
+    import nucleus_sampling_amd as ns
+
+    with pytest.raises(ns.NucleusError):
+        ns.sample_hidden(torch.zeros(2, 8), torch.zeros(16, 8), 1.0, 0.9, uniforms=torch.zeros(2, 1))
+    with pytest.raises(ns.NucleusError):
+        ns.sample_hidden(torch.zeros(2, 8), torch.zeros(16, 8), 1.0, 0.9)
