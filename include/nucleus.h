@@ -409,11 +409,12 @@ size_t nucleus_given_workspace_bytes(int64_t B, int64_t V, int32_t dtype);
  *               d is outside [0, V), if u0, or for a rejected row u1, is NaN,
  *               or if the sum of r is 0 or not finite.
  * out_accepted  device [B] int32, or NULL.
- * opt           required for B > 0: stream and the workspace (at least
- *               nucleus_spec_given_workspace_bytes(B, V) bytes, 256-byte
+ * opt           stream and, where nucleus_spec_given_workspace_bytes(B, V) is
+ *               not 0, the workspace (at least that many bytes, 256-byte
  *               aligned, no initial value needed; NUCLEUS_EWORKSPACE
  *               otherwise) are used; dtype must be NUCLEUS_F32, row_stride 0
- *               or V, everything else unset (NUCLEUS_EINVAL otherwise).
+ *               or V, everything else unset (NUCLEUS_EINVAL otherwise).  NULL:
+ *               the null stream and no workspace.
  *
  * Returns NUCLEUS_OK or a negative code.  Asynchronous on opt->stream, and
  * may be captured into a graph; calls that may overlap need different
@@ -424,7 +425,8 @@ int nucleus_spec_verify_given(const float* target_probs, const float* draft_prob
                               int32_t* out_accepted, const nucleus_options* opt);
 
 /* Device workspace, in bytes, that nucleus_spec_verify_given needs: 8 bytes
- * per 8192-token chunk of every row.  0 for invalid shapes. */
+ * per 8192-token chunk of every row; none for rows of up to 32768 tokens, which
+ * one workgroup each reads in one launch.  0 for invalid shapes. */
 size_t nucleus_spec_given_workspace_bytes(int64_t B, int64_t V);
 
 /* Device workspace, in bytes, that nucleus_spec_verify needs: 8 bytes per

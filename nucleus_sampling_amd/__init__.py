@@ -658,8 +658,8 @@ def _spec_verify_given(handle, dev, target_probs, draft_probs, draft_token, unif
                      _output(o.accepted, (B,), torch.int32, "accepted", dev))
     L = _lib or lib()
     need = L.nucleus_spec_given_workspace_bytes(B, V)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    opt = _Options(0, 0, handle, 0, ws.data_ptr(), need)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    opt = _Options(0, 0, handle, 0, ws.data_ptr() if need else None, need)
     _check(L.nucleus_spec_verify_given(Pt.data_ptr(), Qt.data_ptr(), dp, B, V, U.data_ptr(), ucode,
                                        res.token.data_ptr(), res.accepted.data_ptr(), ctypes.byref(opt)),
            "nucleus_spec_verify_given")

@@ -1918,14 +1918,18 @@ __global__ __launch_bounds__(kPartThreads) void given_probs_kernel(GivenParams p
 // Speculative acceptance from given uniforms: accept d iff u0 q(d) < p(d),
 // else the inverse CDF with u1 over r_i = max(p_i - q_i, 0) in index order.
 //
-// Two launches, as in spec.h: a workgroup per 8192-token chunk of every row
-// sums r over the chunks of rejected rows in doubles (in a fixed order); then
-// a workgroup per row finds the chunk and reads that chunk again.
+// A short row is one workgroup's.  Longer ones take two launches, as in
+// spec.h: a workgroup per 8192-token chunk of every row sums r over the chunks
+// of rejected rows in doubles (in a fixed order); then a workgroup per row
+// finds the chunk and reads that chunk again.
 // ---------------------------------------------------------------------------
 constexpr int kPickThreads = 256;
 constexpr int kPickWaves = kPickThreads / kWave;
 constexpr int kPickSteps = 8;                              // of 64 groups of 4 tokens, per wave
-constexpr int kPickChunk = kPickThreads * kPickSteps * 4;  // 8192 tokens
+constexpr int kPickRun = kPickSteps * kWave * 4;           // 2048 tokens
+constexpr int kPickChunk = kPickWaves * kPickRun;          // 8192 tokens
+constexpr int kPickWide = 1024;                            // threads of pick_row_kernel
+constexpr int kPickShort = kPickWide / kWave * kPickRun;   // 32768 tokens: its rows, at most
 
 struct PickParams {
     const float* target;         // [B, V]: p
@@ -1950,12 +1954,11 @@ __device__ __forceinline__ int pick_verdict(const PickParams& p, int64_t b)
     return u * (double)p.draft[b * p.V + d] < (double)p.target[b * p.V + d] ? 1 : 0;
 }
 
-// max(p - q, 0) of step k's group of this lane in chunk c (0 for NaN and past
-// the row's end).
-__device__ __forceinline__ void pick_load(const PickParams& p, int64_t b, int c, int k, double (&r)[4])
+// max(p - q, 0) of this lane's group in step k of the run of tokens that starts
+// at i (0 for NaN and past the row's end).
+__device__ __forceinline__ void pick_load(const PickParams& p, int64_t b, int64_t i, int k, double (&r)[4])
 {
-    const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-    const int64_t i0 = (int64_t)c * kPickChunk + (int64_t)((w * kPickSteps + k) * kWave + lane) * 4;
+    const int64_t i0 = i + (k * kWave + (int)(threadIdx.x & (kWave - 1))) * 4;
     const float *P = p.target + b * p.V, *Q = p.draft + b * p.V;
     float a[4], e[4];
     if (p.vec && i0 + 4 <= p.V) {
@@ -1989,7 +1992,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_chunk_kernel(PickParams p)
 #pragma unroll
     for (int k = 0; k < kPickSteps; ++k) {
         double r[4];
-        pick_load(p, b, c, k, r);
+        pick_load(p, b, (int64_t)c * kPickChunk + threadIdx.x / kWave * kPickRun, k, r);
         sum += (r[0] + r[1]) + (r[2] + r[3]);
     }
     sum = block_reduce<kPickThreads>(sum, SumF64(), red);
@@ -2040,7 +2043,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_finish_kernel(PickParams p)
         }
         double r[kPickSteps][4], sum = 0.0;
 #pragma unroll
-        for (int k = 0; k < kPickSteps; ++k) pick_load(p, b, chunk, k, r[k]);
+        for (int k = 0; k < kPickSteps; ++k) pick_load(p, b, (int64_t)chunk * kPickChunk + w * kPickRun, k, r[k]);
 #pragma unroll
         for (int k = 0; k < kPickSteps; ++k) sum += (r[k][0] + r[k][1]) + (r[k][2] + r[k][3]);
         sum = wave_reduce(sum, SumF64());
@@ -2082,6 +2085,79 @@ __global__ __launch_bounds__(kPickThreads) void pick_finish_kernel(PickParams p)
             if (found[i] >= 0) token = found[i];
     }
     if (t == 0) {
+        p.out_token[b] = token;
+        if (p.out_accepted) p.out_accepted[b] = 0;
+    }
+}
+
+// A row of up to kPickShort tokens on one workgroup, a run a wave: the wave
+// that holds the draw finds it among what it has in registers.
+__global__ __launch_bounds__(kPickWide) void pick_row_kernel(PickParams p)
+{
+    constexpr int WAVES = kPickWide / kWave;
+    __shared__ double wsum[WAVES];
+    const int64_t b = blockIdx.x;
+    const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+    const double u = p.u_f64 ? ((const double*)p.uniforms)[2 * b + 1] : (double)((const float*)p.uniforms)[2 * b + 1];
+    const int verdict = pick_verdict(p, b);
+    if (verdict != 0) {
+        if (t == 0) {
+            p.out_token[b] = verdict > 0 ? p.draft_token[b] : -1;
+            if (p.out_accepted) p.out_accepted[b] = verdict > 0 ? 1 : 0;
+        }
+        return;
+    }
+    double r[kPickSteps][4], sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < kPickSteps; ++k) pick_load(p, b, (int64_t)w * kPickRun, k, r[k]);
+#pragma unroll
+    for (int k = 0; k < kPickSteps; ++k) sum += (r[k][0] + r[k][1]) + (r[k][2] + r[k][3]);
+    sum = wave_reduce(sum, SumF64());
+    if (lane == 0) wsum[w] = sum;
+    __syncthreads();
+    // Every wave looks at all sums in the same way.
+    double S;
+    const double v = lane < WAVES ? wsum[lane] : 0.0;
+    const double run = wave_inclusive_sum(v, S);
+    const double at = (u < 0.0 ? 0.0 : (u > 1.0 ? 1.0 : u)) * S;
+    const uint64_t mass = __ballot(v > 0.0), over = __ballot(v > 0.0 && run > at);
+    if (!(S > 0.0 && S < (double)INFINITY && u == u)) {
+        if (t == 0) {
+            p.out_token[b] = -1;
+            if (p.out_accepted) p.out_accepted[b] = 0;
+        }
+        return;
+    }
+    // The first run that exceeds `at`, or the last with mass.
+    const int found = over ? (int)__builtin_ctzll(over) : 63 - (int)__builtin_clzll(mass);
+    if (w != found) return;
+    double before = found ? lane_value(run, found - 1) : 0.0;
+    int token = -1;
+    bool open = true;
+#pragma unroll
+    for (int k = 0; k < kPickSteps; ++k) {
+        const int i0 = w * kPickRun + (k * kWave + lane) * 4;
+        double all;
+        const double inc = wave_inclusive_sum((r[k][0] + r[k][1]) + (r[k][2] + r[k][3]), all);
+        const double prev = wave_shift_up1(inc);
+        double a = before + (lane ? prev : 0.0);
+        int tok = -1, end = -1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a += r[k][j];
+            if (r[k][j] > 0.0) {
+                end = i0 + j;
+                if (tok < 0 && a > at) tok = i0 + j;
+            }
+        }
+        const uint64_t hits = __ballot(tok >= 0), ends = __ballot(end >= 0);
+        if (open && ends)
+            token = hits ? __builtin_amdgcn_readlane(tok, (int)__builtin_ctzll(hits))
+                         : __builtin_amdgcn_readlane(end, 63 - (int)__builtin_clzll(ends));
+        if (hits) open = false;
+        before += all;
+    }
+    if (lane == 0) {
         p.out_token[b] = token;
         if (p.out_accepted) p.out_accepted[b] = 0;
     }

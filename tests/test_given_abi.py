@@ -62,15 +62,16 @@ def test_spec_verify_given_argument_errors(L):
     for kw in (dict(dtype=1), dict(dtype=2), dict(row_stride=9), *OTHERS):
         assert _verify(L, opt=_opt(**ws, **kw)) == EINVAL, kw
     assert _verify(L, B=1 << 20, V=1 << 30, opt=_opt(**ws)) == EINVAL  # more chunks than a grid holds
-    assert _verify(L) == EWORKSPACE
-    assert _verify(L, opt=_opt(workspace=1 << 40, workspace_bytes=255)) == EWORKSPACE
-    assert _verify(L, opt=_opt(workspace=(1 << 40) + 128, workspace_bytes=4096)) == EWORKSPACE
+    assert _verify(L, V=40000) == EWORKSPACE
+    assert _verify(L, V=40000, opt=_opt(workspace=1 << 40, workspace_bytes=255)) == EWORKSPACE
+    assert _verify(L, V=40000, opt=_opt(workspace=(1 << 40) + 128, workspace_bytes=4096)) == EWORKSPACE
     assert _verify(L, B=0) == 0
 
 
 def test_spec_given_workspace(L):
     assert L.nucleus_spec_given_workspace_bytes(256, 128256) == 256 * 16 * 8
-    assert L.nucleus_spec_given_workspace_bytes(1, 1) == 256
+    assert L.nucleus_spec_given_workspace_bytes(1, 32769) == 256
+    assert L.nucleus_spec_given_workspace_bytes(500, 32768) == 0  # short rows need none
     assert L.nucleus_spec_given_workspace_bytes(0, 8) == 0
     assert L.nucleus_spec_given_workspace_bytes(-1, 8) == 0 and L.nucleus_spec_given_workspace_bytes(2, 0) == 0
 

@@ -417,3 +417,13 @@ def test_verify_edges():
     q[15, d[15]] = np.nan
     tok, acc = _verify(p, q, d, u, "edges")
     assert (tok[[0, 1, 2, 3, 5, 6, 7]] == -1).all() and tok[12] == 8999
+
+
+@pytest.mark.parametrize("V", [2047, 2048, 2049, 32767, 32768, 32769])
+def test_verify_at_the_sizes_where_its_kernels_change(V):
+    rng = np.random.default_rng(V)
+    p, q = _dists(rng, 40, V)
+    d = rng.integers(0, V, 40).astype(np.int32)
+    u = np.stack([rng.random(40) * 2, np.linspace(0, 1, 40)], 1).astype(np.float32)
+    d[:20] = p[:20].argmin(1)  # (of weight 0, many: rejected)
+    _verify(p, q, d, u, "around a size")
