@@ -15,6 +15,8 @@
 // and the result is rounded once, to the output type.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "params.h"
 
@@ -84,46 +86,90 @@ __device__ __forceinline__ float activate(int act, float cap, float z)
     switch (act) {
     case kActRelu: return z < 0.0f ? 0.0f : z;  // NaN stays
     case kActGelu: return 0.5f * z * erfcf(z * -0.70710678f);
-    case kActSilu: return z / (1.0f + expf(-z));
+    case kActSilu: {
+        // z / (1 + e^-z), with e^-|z| so that nothing overflows and the
+        // reciprocal (off by one unit at most) is of 1 to 2.
+        const float e = expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+        return (z < 0.0f ? z * e : z) * r;
+    }
     case kActSoftcap: return cap * tanhf(z / cap);
     default: return z;
     }
 }
 
-template <int DT>
-__device__ __forceinline__ float load_elem(const void* p, int64_t i, int f32)
+// Four elements of bias or residual as they lie in memory, from element n of
+// the row at `row`; values4 makes numbers of them, so that the load can be far
+// ahead of its use.  VEC: groups of four are whole and aligned; else every
+// element is loaded by itself, past the row's end the last again.
+template <int DT, bool VEC>
+__device__ __forceinline__ u32x4 fetch4(const void* row, int64_t n, int64_t N, int f32)
 {
-    if (DT == kF32 || f32) return ((const float*)p)[i];
-    return (float)((const typename Elem<DT>::T*)p)[i];
+    u32x4 r = {0, 0, 0, 0};
+    if (DT == kF32 || f32) {
+        const uint32_t* at = (const uint32_t*)row;
+        if constexpr (VEC) return *(const u32x4*)(at + n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = at[min(n + j, N - 1)];
+    } else {
+        const uint16_t* at = (const uint16_t*)row;
+        if constexpr (VEC) {
+            const uint2 v = *(const uint2*)(at + n);
+            return u32x4{v.x, v.y, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = at[min(n + j, N - 1)];
+    }
+    return r;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ f32x4 values4(u32x4 r, int f32)
+{
+    if (DT == kF32 || f32) return __builtin_bit_cast(f32x4, r);
+    if constexpr (VEC) r = u32x4{r[0] & 0xFFFFu, r[0] >> 16, r[1] & 0xFFFFu, r[1] >> 16};
+    if constexpr (DT == kBF16) return __builtin_bit_cast(f32x4, r << 16);
+    f32x4 z;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)r[j]);
+    return z;
 }
 
-template <int DT>
-__device__ __forceinline__ f32x4 load_elem4(const void* p, int64_t i, int f32)
+// The raw bias of n .. n + 3 and residual of row m there; any n and m (those
+// past the end read the last, and are not stored).
+template <int DT, bool VEC>
+__device__ __forceinline__ u32x4 fetch_bias(const ProjectParams& p, int64_t n)
 {
-    typedef typename Elem<DT>::T T;
-    typedef T T4 __attribute__((ext_vector_type(4)));
-    if (DT == kF32 || f32) return *(const f32x4*)((const float*)p + i);
-    return __builtin_convertvector(*(const T4*)((const T*)p + i), f32x4);
+    if (!p.bias) return u32x4{0, 0, 0, 0};
+    return fetch4<DT, VEC>(p.bias, n < p.N ? n : 0, p.N, p.bias_f32);
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ u32x4 fetch_residual(const ProjectParams& p, int64_t m, int64_t n)
+{
+    const int64_t at = min(m, p.M - 1) * p.rs;
+    return fetch4<DT, VEC>((const char*)p.res + at * (DT == kF32 || p.res_f32 ? 4 : 2), n < p.N ? n : 0, p.N, p.res_f32);
 }
 
 // Finish and store out[m, n .. n + 3] from their sums; elements past N (and
 // rows past M) are left alone.  A residual that is `out` itself is fine: each
-// element is read by the thread that writes it, before it does.
-template <int DT>
-__device__ __forceinline__ void project_store(const ProjectParams& p, int64_t m, int64_t n, f32x4 z)
+// element is read by the thread that writes it, before it does.  ACT is the
+// activation, or -1 to look at p.act for every element.
+template <int DT, bool VEC, int ACT>
+__device__ __forceinline__ void project_store(const ProjectParams& p, int64_t m, int64_t n, f32x4 z, u32x4 bias,
+                                              u32x4 residual)
 {
     typedef typename Elem<DT>::T T;
     typedef T T4 __attribute__((ext_vector_type(4)));
-    if (m >= p.M || n >= p.N) return;
-    if (p.vec) {
-        if (p.bias) z += load_elem4<DT>(p.bias, n, p.bias_f32);
-        if (p.act != kActNone) {
+    if (p.bias) z += values4<DT, VEC>(bias, p.bias_f32);
+    const int act = ACT < 0 ? p.act : ACT;
+    if (act != kActNone) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) z[r] = activate(p.act, p.cap, z[r]);
-        }
-        if (p.res) z += load_elem4<DT>(p.res, m * p.rs + n, p.res_f32);
-        const int64_t o = m * p.os + n;
-        if (DT == kF32 || p.out_f32)
+        for (int r = 0; r < 4; ++r) z[r] = activate(act, p.cap, z[r]);
+    }
+    if (p.res) z += values4<DT, VEC>(residual, p.res_f32);
+    if (m >= p.M || n >= p.N) return;
+    const int64_t o = m * p.os + n;
+    const bool f32 = DT == kF32 || p.out_f32;
+    if constexpr (VEC) {
+        if (f32)
             *(f32x4*)((float*)p.out + o) = z;
         else
             *(T4*)((T*)p.out + o) = __builtin_convertvector(z, T4);
@@ -131,16 +177,25 @@ __device__ __forceinline__ void project_store(const ProjectParams& p, int64_t m,
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             if (n + r >= p.N) break;
-            float v = z[r];
-            if (p.bias) v += load_elem<DT>(p.bias, n + r, p.bias_f32);
-            v = activate(p.act, p.cap, v);
-            if (p.res) v += load_elem<DT>(p.res, m * p.rs + n + r, p.res_f32);
-            const int64_t o = m * p.os + n + r;
-            if (DT == kF32 || p.out_f32)
-                ((float*)p.out)[o] = v;
+            if (f32)
+                ((float*)p.out)[o + r] = z[r];
             else
-                ((T*)p.out)[o] = (T)v;
+                ((T*)p.out)[o + r] = (T)z[r];
         }
+    }
+}
+
+// The same with the bias and residual asked for here.
+template <int DT>
+__device__ __forceinline__ void finish_group(const ProjectParams& p, int64_t m, int64_t n, f32x4 z)
+{
+    u32x4 residual = {0, 0, 0, 0};
+    if (p.vec) {
+        if (p.res) residual = fetch_residual<DT, true>(p, m, n);
+        project_store<DT, true, -1>(p, m, n, z, fetch_bias<DT, true>(p, n), residual);
+    } else {
+        if (p.res) residual = fetch_residual<DT, false>(p, m, n);
+        project_store<DT, false, -1>(p, m, n, z, fetch_bias<DT, false>(p, n), residual);
     }
 }
 
@@ -216,8 +271,10 @@ __global__ __launch_bounds__(kAnyThreads) void project_any_kernel(ProjectParams 
         for (int u = 0; u < 4; ++u) acc[u] = joined<DT>(acc[u], sum[u]);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-        project_store<DT>(p, m0 + 16 * u + (lane & 15), n0 + 16 * w + 4 * (lane >> 4), acc[u]);
+    for (int u = 0; u < 4; ++u) {
+        const int64_t m = m0 + 16 * u + (lane & 15), n = n0 + 16 * w + 4 * (lane >> 4);
+        finish_group<DT>(p, m, n, acc[u]);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -277,6 +334,50 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t nt, uint32_t mt, u
     const uint32_t rows = min(band, mt - g * band);
     tn = rest / rows;
     tm = g * band + rest % rows;
+}
+
+// Sums in LDS: `rows` rows `pitch` bytes apart; row i is the output's row
+// m0 + (i / run) apart + i % run.
+struct Staged {
+    const char* lds;
+    int pitch, rows, run, apart;
+    int64_t m0;
+};
+
+// Finishes them, BN columns from n0, with NW waves.  A thread's columns are the
+// same in every row it takes, and so is its bias; rows go four at a time with
+// the residuals of the next four on their way.
+template <int DT, bool VEC, int ACT, int BN, int NW, int UP>
+__device__ __forceinline__ void finish_rows(const ProjectParams& p, const Staged& st, int64_t n0)
+{
+    constexpr int COLS = BN / 4, STEP = NW * 64 / COLS;
+    static_assert(NW * 64 % COLS == 0, "a thread keeps its columns");
+    const int col = (int)(threadIdx.x % COLS);
+    const int64_t n = n0 + 4 * col;
+    const auto row_of = [&](int i) { return i < st.rows ? st.m0 + (i / st.run) * st.apart + i % st.run : p.M; };
+    const u32x4 bias = fetch_bias<DT, VEC>(p, n);
+    u32x4 next[UP] = {};
+    const auto fetch = [&](int i) {
+        if (p.res) {  // uniform
+#pragma unroll
+            for (int k = 0; k < UP; ++k) next[k] = fetch_residual<DT, VEC>(p, row_of(i + k * STEP), n);
+        }
+    };
+    int i = threadIdx.x / COLS;
+    fetch(i);
+#pragma unroll 1
+    for (; i < st.rows; i += UP * STEP) {
+        u32x4 residual[UP];
+        f32x4 z[UP];
+#pragma unroll
+        for (int k = 0; k < UP; ++k) {
+            residual[k] = next[k];
+            z[k] = *(const f32x4*)(st.lds + min(i + k * STEP, st.rows - 1) * st.pitch + col * 16);
+        }
+        fetch(i + UP * STEP);
+#pragma unroll
+        for (int k = 0; k < UP; ++k) project_store<DT, VEC, ACT>(p, row_of(i + k * STEP), n, z[k], bias, residual[k]);
+    }
 }
 
 template <int DT, int BN, int BM, int WN, int WM, int STAGES>
@@ -366,21 +467,32 @@ __global__ __launch_bounds__(WN* WM * 64, 1) void project_tile_kernel(ProjectPar
     constexpr int FIT = STAGES * STAGE / (WM * 16 * PITCH);
     constexpr int JG = FIT >= TM ? TM : (FIT >= 4 && TM % 4 == 0 ? 4 : (FIT >= 2 && TM % 2 == 0 ? 2 : 1));
     static_assert(FIT >= 1, "a tile row of every wave fits");
-#pragma unroll
+    constexpr int UP = TN * TM > 16 ? 2 : 4;  // (registers hold the other turns' sums)
+#pragma unroll 1
     for (int j0 = 0; j0 < TM; j0 += JG) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < JG; ++j)
+        for (int now = 0; now < TM; now += JG)
+            if (now == j0) {  // uniform
 #pragma unroll
-            for (int i = 0; i < TN; ++i)
-                *(f32x4*)(lds + ((wm * JG + j) * 16 + r16) * PITCH + ((wn * TN + i) * 16 + 4 * (lane >> 4)) * 4) =
-                    acc[i][j0 + j];
+                for (int j = 0; j < JG; ++j)
+#pragma unroll
+                    for (int i = 0; i < TN; ++i)
+                        *(f32x4*)(lds + ((wm * JG + j) * 16 + r16) * PITCH + ((wn * TN + i) * 16 + 4 * (lane >> 4)) * 4) =
+                            acc[i][now + j];
+            }
         __syncthreads();
-#pragma unroll 1
-        for (int e = threadIdx.x; e < WM * JG * 16 * (BN / 4); e += NW * 64) {
-            const int row = e / (BN / 4), n4 = e % (BN / 4);
-            const int m = ((row / (JG * 16)) * TM + j0) * 16 + row % (JG * 16);
-            project_store<DT>(p, m0 + m, n0 + 4 * n4, *(const f32x4*)(lds + row * PITCH + n4 * 16));
+        const Staged st = {lds, PITCH, WM * JG * 16, JG * 16, TM * 16, m0 + j0 * 16};
+        if (!p.vec) {
+            finish_rows<DT, false, -1, BN, NW, UP>(p, st, n0);
+        } else {
+            switch (p.act) {
+            case kActRelu: finish_rows<DT, true, kActRelu, BN, NW, UP>(p, st, n0); break;
+            case kActGelu: finish_rows<DT, true, kActGelu, BN, NW, UP>(p, st, n0); break;
+            case kActSilu: finish_rows<DT, true, kActSilu, BN, NW, UP>(p, st, n0); break;
+            case kActSoftcap: finish_rows<DT, true, kActSoftcap, BN, NW, UP>(p, st, n0); break;
+            default: finish_rows<DT, true, kActNone, BN, NW, UP>(p, st, n0);
+            }
         }
     }
 }
@@ -442,6 +554,15 @@ __global__ __launch_bounds__(kSplitWaves * 64, 1) void project_split_kernel(Proj
     };
     const int r16 = lane & 15;
     const int f = r16 * 128 + (((lane >> 4) ^ (r16 >> 1)) * 16);
+    // What this thread finishes; its bias and residual arrive under the loop.
+    static_assert(TM * 64 <= kSplitWaves * 64, "one group a thread");
+    const int64_t m = m0 + 16 * (threadIdx.x >> 6) + r16, n = n0 + 4 * (lane >> 4);
+    const bool finishes = (int)threadIdx.x < TM * 64;
+    u32x4 bias = {0, 0, 0, 0}, residual = {0, 0, 0, 0};
+    if (finishes) {
+        bias = p.vec ? fetch_bias<DT, true>(p, n) : fetch_bias<DT, false>(p, n);
+        if (p.res) residual = p.vec ? fetch_residual<DT, true>(p, m, n) : fetch_residual<DT, false>(p, m, n);
+    }
     f32x4 acc[TM] = {};
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s)
@@ -473,12 +594,15 @@ __global__ __launch_bounds__(kSplitWaves * 64, 1) void project_split_kernel(Proj
 #pragma unroll
     for (int j = 0; j < TM; ++j) part[(v * TM + j) * 64 + lane] = acc[j];
     __syncthreads();
-    for (int e = threadIdx.x; e < TM * 64; e += kSplitWaves * 64) {
+    if (finishes) {
+        const int e = threadIdx.x;
         f32x4 z = part[e];
 #pragma unroll
         for (int w = 1; w < kSplitWaves; ++w) z += part[w * TM * 64 + e];
-        const int l = e & 63;
-        project_store<DT>(p, m0 + 16 * (e >> 6) + (l & 15), n0 + 4 * (l >> 4), z);
+        if (p.vec)
+            project_store<DT, true, -1>(p, m, n, z, bias, residual);
+        else
+            project_store<DT, false, -1>(p, m, n, z, bias, residual);
     }
 }
 
