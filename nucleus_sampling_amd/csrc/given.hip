@@ -34,13 +34,14 @@ int64_t parts_of(int64_t V, int32_t dtype)
 // 42 / 35, of 65536 46 / 48, of 128256 50 / 76; 128 rows of 128256 68 / 80).
 // With more rows one workgroup a row fills the device (256 rows of 65536
 // float32 61 / 57, of 128256 bf16 87 / 81).  Float32 rows of 12 parts and more
-// are split at any batch: 256 alike rows of 128256 84 / 85 and 1024 302 / 321,
+// are split up to 1024 rows: 256 alike rows of 128256 84 / 85 and 1024 302 / 321,
 // and where the rows' kept sets differ in size one workgroup waits for the
-// largest (84 / 97).
+// largest (84 / 97).  The workspace, a third of the logits' size there, is why
+// larger batches are not.
 bool split_pays(int64_t B, int64_t V, int32_t dtype)
 {
     const int64_t C = parts_of(V, dtype);
-    return (C >= (dtype == NUCLEUS_F32 ? 6 : 4) && B <= 128) || (C >= 12 && dtype == NUCLEUS_F32);
+    return (C >= (dtype == NUCLEUS_F32 ? 6 : 4) && B <= 128) || (C >= 12 && dtype == NUCLEUS_F32 && B <= 1024);
 }
 
 // Up to this many rows the first pass is split too; from there one workgroup

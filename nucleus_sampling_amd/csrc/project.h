@@ -36,7 +36,7 @@ struct ProjectParams {
     int64_t M, N, K;
     int64_t hs, ws;      // bytes
     int64_t os, rs;      // elements
-    float cap;           // softcap
+    float cap, per_cap;  // softcap; 1 / cap, or 0 where that is no good number
     int act;
     int out_f32, bias_f32, res_f32;
     int vec;             // groups of four n are whole and aligned in out, bias and residual
@@ -81,7 +81,20 @@ __device__ __forceinline__ f32x4 joined(f32x4 acc, f32x4 sum)
     return DT == kF32 ? acc + sum : sum;
 }
 
-__device__ __forceinline__ float activate(int act, float cap, float z)
+// tanh to five units: (1 - e) / (1 + e) with e = e^(-2|x|), and up to 1/4,
+// where that cancels, the series to x^9 (the next term is 9e-9 of x).
+__device__ __forceinline__ float tanh_of(float x)
+{
+    const float e = __builtin_amdgcn_exp2f(fabsf(x) * -2.88539008f), x2 = x * x;
+    const float far = (1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e);
+    float near = fmaf(x2, 62.0f / 2835.0f, -17.0f / 315.0f);
+    near = fmaf(x2, near, 2.0f / 15.0f);
+    near = fmaf(x2, near, -1.0f / 3.0f);
+    near = fmaf(x2 * x, near, x);
+    return fabsf(x) < 0.25f ? near : copysignf(far, x);
+}
+
+__device__ __forceinline__ float activate(int act, float cap, float per_cap, float z)
 {
     switch (act) {
     case kActRelu: return z < 0.0f ? 0.0f : z;  // NaN stays
@@ -92,7 +105,8 @@ __device__ __forceinline__ float activate(int act, float cap, float z)
         const float e = expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
         return (z < 0.0f ? z * e : z) * r;
     }
-    case kActSoftcap: return cap * tanhf(z / cap);
+    // (a product with the reciprocal moves the argument by one unit at most)
+    case kActSoftcap: return cap * tanh_of(per_cap != 0.0f ? z * per_cap : z / cap);
     default: return z;
     }
 }
@@ -162,7 +176,7 @@ __device__ __forceinline__ void project_store(const ProjectParams& p, int64_t m,
     const int act = ACT < 0 ? p.act : ACT;
     if (act != kActNone) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) z[r] = activate(act, p.cap, z[r]);
+        for (int r = 0; r < 4; ++r) z[r] = activate(act, p.cap, p.per_cap, z[r]);
     }
     if (p.res) z += values4<DT, VEC>(residual, p.res_f32);
     if (m >= p.M || n >= p.N) return;

@@ -174,6 +174,7 @@ extern "C" int nucleus_project(const void* hidden, const void* weight, int64_t M
     p.os = os;
     p.rs = rs;
     p.cap = o.softcap;
+    p.per_cap = o.softcap > 0x1p-100f && o.softcap < 0x1p100f ? 1.0f / o.softcap : 0.0f;
     p.act = o.activation;
     p.out_f32 = o.out_dtype == NUCLEUS_F32;
     p.bias_f32 = o.bias_dtype == NUCLEUS_F32;
