@@ -49,7 +49,7 @@
 // comes from cache.  A row of 128256 float32 logits, all 256 CUs at work: first
 // pass 26 us (131 MB at 5 TB/s), cells of the cuts 3, second pass 5 to 57 by the
 // size of the nucleus, exact level 5, a round of eight draws 4.  Rows of 1024:
-// 3, 3, 2, 5 and 3 us, all of them waits on one another.
+// 3, 3, 2, 2 and 3 us, all of them waits on one another.
 #pragma once
 
 #include <type_traits>
@@ -397,6 +397,9 @@ struct GivenShared {
     uint32_t n_above, n_window;
     int cross;
     uint64_t tc;
+    // a few undecided tokens, on one wave
+    uint2 few[kWave];
+    uint32_t few_n, few_cut;
 };
 
 struct SumF64 { __device__ double operator()(double a, double b) const { return a + b; } };
@@ -757,6 +760,33 @@ __device__ __forceinline__ void store_single(const GivenParams& p, int64_t b, in
     }
 }
 
+// Is x one of the undecided?  (NaN, an empty place's, is not.)
+__device__ __forceinline__ bool is_undecided(const RowPlan& o, float x, int& r, double& h)
+{
+    if (!(x >= o.floor_x)) return false;
+    r = rank_of(o, x, h);
+    return r >= o.r_lo && (r <= o.r_hi || r == o.rb);
+}
+
+// Copies the undecided of a list of ln <= NT places to sh.few, as many as it
+// holds, and counts them in sh.few_n.
+template <class Shared>
+__device__ __forceinline__ void gather_few(Shared& sh, const RowPlan& o, uint32_t ln)
+{
+    const uint32_t t = threadIdx.x;
+    const uint2 e = sh.list[t < ln ? t : 0];
+    int r;
+    double h;
+    const bool mine = t < ln && is_undecided(o, __uint_as_float(e.x), r, h);
+    const uint64_t all = lanes(mine);
+    if (all) {  // uniform
+        uint32_t at = 0;
+        if ((t & (kWave - 1)) == 0) at = atomicAdd(&sh.few_n, (uint32_t)__builtin_popcountll(all));
+        at = uniform(at) + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+        if (mine && at < kWave) sh.few[at] = e;
+    }
+}
+
 // The exact cut: the logit at and above which a row's finite tokens are kept.
 // The undecided tokens are in sh.list (`listed`: `ln` places) or read from the
 // row again; kmin, kmax: this thread's least and largest key of those that
@@ -787,10 +817,9 @@ __device__ __forceinline__ float resolve_row(Shared& sh, const GivenParams& p, c
                 } else {
                     x = logit_at<DT>(row, i);
                 }
-                if (!(x >= o.floor_x)) continue;
+                int r;
                 double h;
-                const int r = rank_of(o, x, h);
-                if (r >= o.r_lo && (r <= o.r_hi || r == o.rb)) fn(x, idx, r, h);
+                if (is_undecided(o, x, r, h)) fn(x, idx, r, h);
             }
         };
         // Keys that bound those of rank r's cell (a tenth of a cell to spare).
@@ -817,9 +846,87 @@ __device__ __forceinline__ float resolve_row(Shared& sh, const GivenParams& p, c
                 sh.red64);
             if ((uint32_t)(both >> 32) == ~(uint32_t)both) one_key = (uint32_t)(both >> 32);
         }
+        // The crossing cell, the first whose running mass reaches p S, and the
+        // mass that it is crossed at.
+        auto crossing = [&](double s_bottom, int& cell, uint64_t& thr) {
+            const double want = (double)in.P * (sh.s_above + s_bottom);
+            double a = sh.a_lo, at = sh.a_lo;
+            cell = o.r_lo;
+#pragma unroll 1
+            for (int r = o.r_lo; r <= o.r_hi; ++r) {
+                const double wr =
+                    r == o.rb ? s_bottom : rank_weight(sh.root, r) * ((double)sh.hist[o.top - r] * inv_scale);
+                if (wr > 0.0) {
+                    cell = r;
+                    at = a;
+                    if (a + wr >= want) break;
+                }
+                a += wr;
+            }
+            const double q = (want - at) / (rank_weight(sh.root, cell) * inv_scale);
+            thr = !(q > 1.0) ? 1 : (q < 1.8e19 ? (uint64_t)ceil(q) : ~0ull);
+        };
+        // A kept one: to its segment.
+        auto keep = [&](float x, uint32_t idx) {
+            const uint32_t step = idx / (GN * kWave), own = step / d.steps;
+            atomicAdd((unsigned long long*)&sh.subc[own * d.spw + (step - own * d.steps) / d.sps],
+                      (unsigned long long)fixed_point(mass_of(o, sh.root, x) * scale));
+            ++count;
+        };
         const uint32_t from_minp = order_key(fmaxf(o.tmp, kLowest));
         uint32_t bottom = from_minp;  // lowest key that survives min-p and top-k
         double s_bottom = 0.0;        // mass of the bottom cell's survivors
+        const uint64_t thr_k = in.use_k && sh.n_above < (uint32_t)in.K ? (uint64_t)in.K - sh.n_above : 0;
+        if (listed && ln <= NT) {
+            // At most 64 of them, as in short rows: the first wave has one in
+            // every lane, and compares them all (15 rows of 1024: 18.6 -> 15.6 us).
+            const int lane = t & (kWave - 1);
+            gather_few(sh, o, ln);
+            __syncthreads();
+            const uint32_t n = uniform(sh.few_n);
+            if (n <= kWave) {
+                if (t < kWave) {
+                    const bool have = (uint32_t)lane < n;
+                    const float x = have ? __uint_as_float(sh.few[lane].x) : 0.0f;
+                    double h;
+                    const int rank = rank_of(o, have ? x : o.m, h);
+                    const uint32_t key = order_key(x);
+                    const uint64_t w = fx(h);
+                    // The lowest level above which the cell's tokens weigh less than thr.
+                    auto level_in = [&](int cell, uint64_t weight, uint64_t thr) {
+                        const bool here = have && rank == cell && key >= bottom && weight;
+                        const uint64_t all = lanes(here);
+                        uint64_t above = 0;
+#pragma unroll 1
+                        for (uint64_t m = all; m; m &= m - 1) {
+                            const int j = (int)__builtin_ctzll(m);
+                            const uint64_t wj = lane_read64(weight, j);
+                            if ((uint32_t)__builtin_amdgcn_readlane((int)key, j) > key) above += wj;
+                        }
+                        const uint32_t level = wave_reduce(here && above < thr ? key : 0xFFFFFFFFu, MinU32());
+                        return all ? level : 0u;
+                    };
+                    if (o.rb != kRankNone) {
+                        if (thr_k) bottom = max(bottom, level_in(o.rb, 1, thr_k));
+                        if (o.rb <= o.top && cut_p) {
+                            const uint64_t sum =
+                                wave_reduce(have && rank == o.rb && key >= bottom ? w : (uint64_t)0, SumU64());
+                            s_bottom = rank_weight(sh.root, o.rb) * ((double)sum * inv_scale);
+                        }
+                    }
+                    if (cut_p) {
+                        int cell;
+                        uint64_t thr;
+                        crossing(s_bottom, cell, thr);
+                        bottom = max(bottom, level_in(cell, w, thr));
+                    }
+                    if (have && key >= bottom) keep(x, sh.few[lane].y);
+                    if (t == 0) sh.few_cut = bottom;
+                }
+                __syncthreads();
+                return key_value(uniform(sh.few_cut));
+            }
+        }
         // First the bottom cell by top-k (each token counts 1), then the
         // crossing cell by top-p (each token counts its weight).
 #pragma unroll 1
@@ -829,29 +936,10 @@ __device__ __forceinline__ float resolve_row(Shared& sh, const GivenParams& p, c
             if (step == 0) {
                 if (o.rb == kRankNone) continue;
                 cell = o.rb;
-                thr = in.use_k && sh.n_above < (uint32_t)in.K ? (uint64_t)in.K - sh.n_above : 0;
+                thr = thr_k;
             } else {
                 if (!cut_p) break;
-                if (t == 0) {
-                    // The crossing cell: the first whose running mass reaches p S.
-                    const double want = (double)in.P * (sh.s_above + s_bottom);
-                    double a = sh.a_lo, at = sh.a_lo;
-                    int found = o.r_lo;
-#pragma unroll 1
-                    for (int r = o.r_lo; r <= o.r_hi; ++r) {
-                        const double wr =
-                            r == o.rb ? s_bottom : rank_weight(sh.root, r) * ((double)sh.hist[o.top - r] * inv_scale);
-                        if (wr > 0.0) {
-                            found = r;
-                            at = a;
-                            if (a + wr >= want) break;
-                        }
-                        a += wr;
-                    }
-                    const double q = (want - at) / (rank_weight(sh.root, found) * inv_scale);
-                    sh.cross = found;
-                    sh.tc = !(q > 1.0) ? 1 : (q < 1.8e19 ? (uint64_t)ceil(q) : ~0ull);
-                }
+                if (t == 0) crossing(s_bottom, sh.cross, sh.tc);
                 __syncthreads();
                 cell = uniform(sh.cross);
                 thr = sh.tc;
@@ -891,12 +979,7 @@ __device__ __forceinline__ float resolve_row(Shared& sh, const GivenParams& p, c
         } else {
             // The kept among them, added to their segments.
             undecided([&](float x, uint32_t idx, int, double) {
-                if (order_key(x) >= cut) {
-                    const uint32_t step = idx / (GN * kWave), own = step / d.steps;
-                    atomicAdd((unsigned long long*)&sh.subc[own * d.spw + (step - own * d.steps) / d.sps],
-                              (unsigned long long)fixed_point(mass_of(o, sh.root, x) * scale));
-                    ++count;
-                }
+                if (order_key(x) >= cut) keep(x, idx);
             });
         }
         __syncthreads();
@@ -1123,7 +1206,7 @@ __device__ __forceinline__ void whole_row(Shared& sh, const GivenParams& p, int6
     sh.sub[t] = 0.0;
     sh.pre[t] = 0.0;
     sh.subc[t] = 0;
-    if (t == 0) sh.list_n = 0;
+    if (t == 0) sh.list_n = sh.few_n = 0;
 
     Cells c;
     FirstPass f;
@@ -1346,7 +1429,7 @@ __global__ __launch_bounds__(NT) void given_row_kernel(GivenParams p)
 //
 // Parts of 32 KB put a row of 128256 float32 logits on 16 workgroups and keep
 // LDS small enough for 7 waves a SIMD (64 KB parts of 512 threads: 36 us for
-// the masses of 256 rows, 32 KB 33).  One such row: 6.4, 11, 8, 17 and with
+// the masses of 256 rows, 32 KB 33).  One such row: 6.5, 11, 8, 15 and with
 // probabilities 5.5 us; 256 rows: first pass 32, masses 33, draws 19 us.
 //
 // Launch boundaries are the only joins, so nothing waits inside a kernel and
@@ -1864,6 +1947,7 @@ __global__ __launch_bounds__(NT) void given_draw_kernel(GivenParams p, GivenWork
             for (uint32_t i = t; i < Shared::kCap; i += NT) sh.list[i].x = kEmpty;
         }
     }
+    if (t == 0) sh.few_n = 0;
     __syncthreads();
     double one_weight;
     const Fixed fx(ldexp(1.0, p.bits));

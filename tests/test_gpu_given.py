@@ -234,6 +234,30 @@ def test_max_above_the_window():
     _check(x, T, p, k, None, _u(rng, 4, 4), what="max above the window")
 
 
+@pytest.mark.parametrize("V", [400, 50000])
+def test_about_as_many_undecided_tokens_as_a_wave_has_lanes(V):
+    """62 to 67 tokens in the cells that the cuts fall into, distinct or in
+    ties, cut by top-k, min-p, top-p and pairs of them."""
+    rng = np.random.default_rng(V + 1)
+    x = rng.normal(-9, 1, (36, V)).astype(np.float32)
+    T, p = np.ones(36, np.float32), np.ones(36, np.float32)
+    k, mp = np.zeros(36, np.int32), np.zeros(36, np.float32)
+    for b in range(36):
+        c = 62 + b % 6
+        at = rng.choice(V, c, replace=False)
+        x[b, at] = (np.linspace(0, 0.01, c) if b % 4 else np.round(np.linspace(0, 0.01, c), 3))[rng.permutation(c)]
+        kind = b // 6
+        if kind in (0, 3, 5):
+            p[b] = 0.5
+        if kind in (1, 3):
+            k[b] = c // 2 + 3
+        if kind in (2, 5):
+            mp[b] = 0.996
+        if kind == 4:
+            k[b], p[b] = 1 + b % 3, 0.01
+    _check(x, T, p, k, mp, _u(rng, 36, 3), what="a wave of undecided tokens", strict=False)
+
+
 @pytest.mark.parametrize("dtype,V", [("f32", 45001), ("bf16", 50000)])
 @pytest.mark.parametrize("B", [3, 36])
 def test_every_kind_of_row_in_a_split_batch(B, dtype, V):
