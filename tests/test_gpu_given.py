@@ -451,3 +451,27 @@ def test_verify_at_the_sizes_where_its_kernels_change(V):
     u = np.stack([rng.random(40) * 2, np.linspace(0, 1, 40)], 1).astype(np.float32)
     d[:20] = p[:20].argmin(1)  # (of weight 0, many: rejected)
     _verify(p, q, d, u, "around a size")
+
+
+def test_many_draws_of_split_rows():
+    rng = np.random.default_rng(31)
+    x = rng.normal(0, 2, (2, 60000)).astype(np.float32)
+    _check(x, np.asarray([0.7, 1.1], np.float32), np.asarray([0.9, 1.0], np.float32), None, None,
+           _u(rng, 2, 300, np.float64), what="many draws of split rows", strict=False)
+
+
+def test_empty_batches():
+    import nucleus_sampling_amd as ns
+
+    say("empty batches")
+    none = torch.empty(0, 64, device="cuda")
+    e = torch.empty(0, device="cuda")
+    got = ns.sample_given(none, e, e, torch.empty(0, 3, device="cuda"), want_probs=True)
+    assert got.token.shape == (0, 3) and got.keep_count.shape == (0,) and got.probs.shape == (0, 64)
+    v = ns.spec_verify_given(none, none, torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, 2, device="cuda"))
+    assert v.token.shape == (0,) and v.accepted.shape == (0,)
+    w = torch.zeros(64, 8, device="cuda")
+    assert ns.project(torch.empty(0, 8, device="cuda"), w).shape == (0, 64)
+    assert ns.sample_hidden(torch.empty(0, 8, device="cuda"), w, e, e, uniforms=e).token.shape == (0,)
+    with pytest.raises(ns.NucleusError):
+        ns.sample_given(torch.empty(2, 0, device="cuda"), torch.ones(2), torch.ones(2), torch.zeros(2))
